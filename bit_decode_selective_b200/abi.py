@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_int, c_int32, c_int64, c_size_t, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libsf.so")
@@ -41,6 +41,12 @@ class sf_kv(ctypes.Structure):
                 ("kb", c_void_p), ("kr", c_void_p), ("vb", c_void_p), ("vr", c_void_p),
                 ("ksz", c_void_p), ("vsz", c_void_p)]
 
+
+class sf_kvp(ctypes.Structure):
+    _fields_ = [("n_pages", c_int32), ("page", c_int32), ("h_kv", c_int32), ("d", c_int32), ("pool", c_void_p)]
+
+
+SF_F16, SF_BF16, SF_F32 = range(3)  # sf_dtype
 
 _SIGNATURES = {
     "sf_abi_version": ([], c_int),
@@ -81,6 +87,14 @@ _SIGNATURES = {
     "sf_kv_attend_selective_workspace_bytes": ([POINTER(sf_kv), c_int, c_int, c_int, c_int], c_size_t),
     "sf_kv_attend_selective_static": ([POINTER(sf_kv), c_int, c_void_p, c_int, c_int, c_void_p, c_void_p,
                                        c_void_p, c_void_p], c_int),
+    "sf_kvp_bytes": ([c_int] * 4 + [POINTER(c_size_t)], c_int),
+    "sf_kvp_write": ([POINTER(sf_kvp), c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int, c_int,
+                      c_void_p, c_void_p, c_void_p], c_int),
+    "sf_kvp_read": ([POINTER(sf_kvp), c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p], c_int),
+    "sf_kvp_attend": ([POINTER(sf_kvp), c_void_p, c_int64, c_int64, c_int, c_int, c_void_p, c_void_p, c_int,
+                       c_void_p, c_int, c_int, ctypes.c_float, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                       c_size_t, c_void_p], c_int),
+    "sf_kvp_attend_workspace_bytes": ([POINTER(sf_kvp), c_int, c_int, c_int], c_size_t),
     "sf_rmsnorm_residual": ([c_void_p, c_void_p, c_void_p, c_int, c_int, ctypes.c_float, c_void_p,
                              c_void_p], c_int),
     "sf_rope_split": ([c_void_p, c_int, c_int, c_int, c_int, c_int, ctypes.c_float, c_void_p, c_void_p,
@@ -163,6 +177,11 @@ sf_kv_attend_selective = _call("sf_kv_attend_selective")
 sf_kv_attend_selective_f16 = _call("sf_kv_attend_selective_f16")
 sf_kv_attend_selective_workspace_bytes = _call("sf_kv_attend_selective_workspace_bytes")
 sf_kv_attend_selective_static = _call("sf_kv_attend_selective_static")
+sf_kvp_bytes = _call("sf_kvp_bytes")
+sf_kvp_write = _call("sf_kvp_write")
+sf_kvp_read = _call("sf_kvp_read")
+sf_kvp_attend = _call("sf_kvp_attend")
+sf_kvp_attend_workspace_bytes = _call("sf_kvp_attend_workspace_bytes")
 sf_rmsnorm_residual = _call("sf_rmsnorm_residual")
 sf_rope_split = _call("sf_rope_split")
 sf_silu_mul = _call("sf_silu_mul")

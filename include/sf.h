@@ -381,6 +381,91 @@ SF_API sf_status sf_kv_attend_selective_static(const sf_kv* kv, int t, const uin
                                                sf_stream_t stream);
 
 /* ======================================================================== */
+/* Paged 4-bit KV cache                                                      */
+/* ======================================================================== */
+
+/* Element types of the paged cache's inputs and outputs. */
+typedef enum { SF_F16 = 0, SF_BF16 = 1, SF_F32 = 2 } sf_dtype;
+
+/* A pool of `n_pages` pages of `page` tokens, shared by any number of
+ * sequences ([ABS]: low-bit KV caches; the pages leave the placement open).
+ * Each token and KV head is quantised to plain 4-bit codes (the quantisation
+ * at the top of this file with b = 4, r = 0) in groups of 32 consecutive
+ * elements, with two departures: a NaN counts as 0, and values are first
+ * clamped to +-65408, so that every stored grid stays finite in fp16.
+ *   d in {64, 128}; page a power of two, 16 <= page <= 1024;
+ *   n_pages * page < 2^31.  With G = d / 32:
+ * pool [n_pages][h_kv][page / 16] tiles of 16 tokens, 20 d bytes each:
+ *   key codes   [G][16 tokens][16 bytes]  (element e of the group in nibble e)
+ *   value codes [G][16 tokens][16 bytes]
+ *   key grid    [16 tokens][G][2] fp16    (s, m)
+ *   value grid  [8 token pairs][G][4] fp16 (s of the even token, s of the odd
+ *               one, m of the even one, m of the odd one)
+ * A token owns its bytes: tokens are written independently of one another.
+ * Token slot t = page_index * page + place in the page (int32). */
+typedef struct {
+  int32_t n_pages, page, h_kv, d;
+  void* pool;
+} sf_kvp;
+
+SF_API sf_status sf_kvp_bytes(int n_pages, int page, int h_kv, int d, size_t* bytes);
+
+/* Quantise n tokens and store them in their slots.
+ *   k, v (either may be NULL to skip it): token i's head h starts at element
+ *     i * row + h * head of the pointer and has d consecutive elements of type
+ *     `dtype`; pointers 16-byte aligned, row and head whole multiples of 16
+ *     bytes (views of a fused projection's output are fine);
+ *   slots [n] int32 DEVICE.  -1: the token is skipped (padding).  Any other
+ *     slot outside the pool is not written either and, when `bad` (nullable, a
+ *     device int32) is given, *bad is incremented once for it (the caller
+ *     zeroes it and reads it back).  The slots >= 0 of one call are distinct:
+ *     a slot that several tokens name holds an unspecified mixture of them
+ *     afterwards (no other slot is touched). */
+SF_API sf_status sf_kvp_write(const sf_kvp* kv, const void* k, int64_t k_row, int64_t k_head, const void* v,
+                              int64_t v_row, int64_t v_head, sf_dtype dtype, int n, const int32_t* slots,
+                              int32_t* bad, sf_stream_t stream);
+
+/* The values of n slots: k, v [n][h_kv][d] of type `dtype` (either may be
+ * NULL), m + s q rounded once to fp32 and from there to the type.  slots as in
+ * sf_kvp_write, in any order and repeated at will; the rows of -1 and of slots
+ * outside the pool are filled with zeros (the latter counted in *bad). */
+SF_API sf_status sf_kvp_read(const sf_kvp* kv, const int32_t* slots, int n, void* k, void* v, sf_dtype dtype,
+                             int32_t* bad, sf_stream_t stream);
+
+/* Attention of ragged queries over their sequences' cached tokens:
+ *   out[i][h] = sum_j softmax_j(scale * q[i][h] . k^[j]) v^[j]
+ * over the tokens j of i's sequence that i sees, k^, v^ the stored values of
+ * KV head h / (h_q / h_kv).  Query i of n queries of a sequence of len tokens
+ * stands at position p = len - n + i (the sequence's last n tokens are its
+ * queries' own), and sees
+ *   j <= p  and  (window == 0  or  j > p - window  or  j < sinks):
+ * the window tokens up to its own and the first `sinks` tokens.  A query that
+ * sees nothing (p < 0) gets zeros.
+ *   q [n_q][h_q][d] of type `dtype` (SF_F16 or SF_BF16) with strides q_row,
+ *     q_head as in sf_kvp_write; out [n_q][h_q][d] contiguous, same type;
+ *   cu_q (nullable) [batch + 1] int32 DEVICE, ascending: sequence b's queries
+ *     are rows cu_q[b] .. cu_q[b+1] - 1.  Rows outside every sequence's are
+ *     left as they were.  NULL: every sequence has n_q / batch of them.
+ *   pages [batch][max_pages] int32 DEVICE: page of tokens page*j .. of the
+ *     sequence; only entries that hold visible tokens are read;
+ *   lens [batch] int32 DEVICE: cached tokens per sequence, the queries' own
+ *     included.
+ *   h_q % h_kv == 0; scale finite; window, sinks >= 0.
+ * Device-side arguments are checked there: a length is clamped to [0,
+ * max_pages * page], cu_q to [0, n_q], and the tokens of a page index outside
+ * [0, n_pages) are not read and not seen; each makes *bad (nullable, a device
+ * int32) nonzero.
+ * q must be finite in every row that is to be finite: a row with a NaN or an
+ * infinity spoils its own output only.
+ * ws: sf_kvp_attend_workspace_bytes() bytes, 16-byte aligned, contents
+ * irrelevant before and after; calls that overlap on the GPU need one each. */
+SF_API sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_row, int64_t q_head, sf_dtype dtype,
+                               int n_q, const int32_t* cu_q, const int32_t* pages, int max_pages,
+                               const int32_t* lens, int batch, int h_q, float scale, int window, int sinks,
+                               void* out, int32_t* bad, void* ws, size_t ws_bytes, sf_stream_t stream);
+SF_API size_t sf_kvp_attend_workspace_bytes(const sf_kvp* kv, int n_q, int batch, int h_q);
+
+/* ======================================================================== */
 /* Refinement staging ([EXPL] "the map app also loads tiles": fetch lead)    */
 /* ======================================================================== */
 
