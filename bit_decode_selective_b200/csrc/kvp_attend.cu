@@ -3,51 +3,25 @@
 #include <climits>
 #include <cmath>
 
-#include "kvp.cuh"
+#include "kvp_attend.cuh"
 
 namespace sf {
 namespace {
 
-struct AttendArgs {
-  const uint8_t* pool;
-  const void* q;
-  void* out;
-  int64_t q_row, q_head;
-  const int32_t *cu_q, *pages, *lens;
-  int32_t* bad;
-  int n_pages, page_shift, h_kv, h_q, group;  // group: query heads per KV head
-  int n_q, batch, max_pages, window, sinks;
-  float scale_log2;  // scale * log2(e)
-};
+// Sequences of at most this many rows (queries x query heads per KV head) go to
+// the few-row kernel.
+constexpr int kFewRows = 64;
 
-__device__ __forceinline__ void note_bad(int32_t* bad) {
-  if (bad) atomicAdd(bad, 1);
-}
-
-// Sequence b's query rows [q0, q0 + n) and its length, clamped to what the call
-// can hold.
-__device__ __forceinline__ void sequence(const AttendArgs& a, int b, int& q0, int& n, int& len) {
-  int q1;
-  if (a.cu_q) {
-    q0 = a.cu_q[b], q1 = a.cu_q[b + 1];
-    const int c0 = min(max(q0, 0), a.n_q), c1 = min(max(q1, c0), a.n_q);
-    if (c0 != q0 || c1 != q1) note_bad(a.bad);
-    q0 = c0, q1 = c1;
-  } else {
-    const int per = a.n_q / a.batch;
-    q0 = b * per, q1 = q0 + per;
-  }
-  n = q1 - q0;
-  const long cap = (long)a.max_pages << a.page_shift;
-  const int l = a.lens[b];
-  len = l < 0 ? 0 : (int)min((long)l, cap);
-  if (len != l) note_bad(a.bad);
+// Rows that a sequence of the few-row kernel is expected to have: the average.
+int few_rows(int n_q, int batch, int group) {
+  const long long rows = ((long long)n_q + batch - 1) / batch * group;
+  return rows < kFewRows ? (int)rows : kFewRows;
 }
 
 // One warp per (query, head), a token per lane and step for the logits, D / 32
 // elements per lane for the output.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kvp_attend_plain_kernel(AttendArgs a) {
+__global__ void __launch_bounds__(128) kvp_attend_plain_kernel(KvpAttendArgs a) {
   using L = KvpTile<D>;
   constexpr int E = D / 32;
   __shared__ float qs[4][D];
@@ -55,8 +29,9 @@ __global__ void __launch_bounds__(128) kvp_attend_plain_kernel(AttendArgs a) {
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z;
-  int q0, n, len;
-  sequence(a, b, q0, n, len);
+  const KvpSeq seq = kvp_seq(a, b);
+  const int q0 = seq.q0, n = seq.n, len = seq.len;
+  if ((long)n * a.group <= a.few_rows) return;
   const long unit = (long)blockIdx.x * 4 + warp;
   const int i = (int)(unit / a.h_q), h = (int)(unit % a.h_q), g = h / a.group;
   if (i >= n) return;
@@ -91,7 +66,7 @@ __global__ void __launch_bounds__(128) kvp_attend_plain_kernel(AttendArgs a) {
             x = fmaf(qs[warp][grp * 32 + e], fmaf((float)((w[e >> 3] >> (4 * (e & 7))) & 15u), s, m), x);
         }
       } else {
-        note_bad(a.bad);
+        kvp_note_bad(a.bad);
       }
     }
     float top = x;
@@ -131,7 +106,7 @@ __global__ void __launch_bounds__(128) kvp_attend_plain_kernel(AttendArgs a) {
 }
 
 template <typename T, int D>
-sf_status launch_attend(const AttendArgs& a, cudaStream_t s) {
+sf_status launch_attend(const KvpAttendArgs& a, cudaStream_t s) {
   const long units = (long)(a.cu_q ? a.n_q : a.n_q / a.batch) * a.h_q;
   SF_CUDA(launch_pdl(kvp_attend_plain_kernel<T, D>, dim3((unsigned)((units + 3) / 4), 1, a.batch), dim3(128), 0, s, a));
   return SF_OK;
@@ -153,8 +128,8 @@ sf_status check_attend(const sf_kvp* kv, int n_q, int batch, int h_q) {
 using namespace sf;
 
 extern "C" size_t sf_kvp_attend_workspace_bytes(const sf_kvp* kv, int n_q, int batch, int h_q) {
-  if (check_attend(kv, n_q, batch, h_q) != SF_OK) return 0;
-  return 0;
+  if (check_attend(kv, n_q, batch, h_q) != SF_OK || n_q == 0) return 0;
+  return kvp_decode_workspace(kv->d, few_rows(n_q, batch, h_q / kv->h_kv));
 }
 
 extern "C" sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_row, int64_t q_head, sf_dtype dtype,
@@ -178,19 +153,30 @@ extern "C" sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_ro
   SF_REQUIRE(q_row >= 0 && q_head >= 0 && q_row % 8 == 0 && q_head % 8 == 0,
              "q strides (%lld, %lld) must be whole multiples of 16 bytes", (long long)q_row, (long long)q_head);
   const size_t need = sf_kvp_attend_workspace_bytes(kv, n_q, batch, h_q);
-  if (need > 0 && (!ws || ws_bytes < need)) {
-    set_error("workspace of %zu bytes is smaller than the %zu needed", ws ? ws_bytes : (size_t)0, need);
+  if (!ws || ws_bytes < need) {
+    set_error("workspace: need %zu bytes, got %zu", need, ws ? ws_bytes : (size_t)0);
     return SF_ERR_WORKSPACE;
   }
   SF_REQUIRE(aligned16(ws), "ws must be 16-byte aligned");
-  AttendArgs a = {};
+  KvpAttendArgs a = {};
   a.pool = (const uint8_t*)kv->pool, a.q = q, a.out = out, a.q_row = q_row, a.q_head = q_head;
   a.cu_q = cu_q, a.pages = pages, a.lens = lens, a.bad = bad;
   a.n_pages = kv->n_pages, a.h_kv = kv->h_kv, a.h_q = h_q, a.group = h_q / kv->h_kv;
   while ((1 << a.page_shift) < kv->page) a.page_shift++;
-  a.n_q = n_q, a.batch = batch, a.max_pages = max_pages, a.window = window, a.sinks = sinks;
+  a.n_q = n_q, a.batch = batch, a.max_pages = max_pages, a.sinks = sinks;
+  a.window = window < (long long)max_pages * kv->page ? window : 0;  // as wide as any sequence: no window
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.few_rows = kFewRows;
+  a.ws = ws;
   cudaStream_t s = as_stream(stream);
+  // without cu_q every sequence has the same number of rows; with it the
+  // kernels take the sequences that are theirs
+  const long long each = (long long)(n_q / batch) * a.group;
+  if (cu_q || each <= kFewRows) {
+    const sf_status e = launch_kvp_decode(a, kv->d, dtype, few_rows(n_q, batch, a.group), s);
+    if (e != SF_OK) return e;
+  }
+  if (cu_q ? (long long)n_q * a.group <= kFewRows : each <= kFewRows) return SF_OK;
   if (kv->d == 128)
     return dtype == SF_F16 ? launch_attend<__half, 128>(a, s) : launch_attend<__nv_bfloat16, 128>(a, s);
   return dtype == SF_F16 ? launch_attend<__half, 64>(a, s) : launch_attend<__nv_bfloat16, 64>(a, s);
