@@ -1545,6 +1545,9 @@ extern "C" sf_status sf_device_wait_timeouts(unsigned int* count, int reset) {
     const unsigned int zero = 0;
     SF_CUDA(cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(unsigned int)));
   }
+  unsigned int paged = 0;
+  SF_CUDA(kvp_wait_timeouts(&paged, reset != 0));
+  *count += paged;
   if (*count) {
     set_error("%u bounded device wait(s) ran out", *count);
     return SF_ERR_TIMEOUT;

@@ -13,4 +13,7 @@ sf_status check_select_args(const uint16_t* x, int batch, int k, int chunk, int 
 sf_status launch_select(const uint16_t* x, int batch, int k, int chunk, int kch, int32_t* sel,
                         cudaStream_t s, bool pdl);
 
+// Waits of the paged-cache attention that ran out (kvp_prefill.cu); reset: back to 0.
+cudaError_t kvp_wait_timeouts(unsigned int* count, bool reset);
+
 }  // namespace sf

@@ -18,100 +18,6 @@ int few_rows(int n_q, int batch, int group) {
   return rows < kFewRows ? (int)rows : kFewRows;
 }
 
-// One warp per (query, head), a token per lane and step for the logits, D / 32
-// elements per lane for the output.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) kvp_attend_plain_kernel(KvpAttendArgs a) {
-  using L = KvpTile<D>;
-  constexpr int E = D / 32;
-  __shared__ float qs[4][D];
-  pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.z;
-  const KvpSeq seq = kvp_seq(a, b);
-  const int q0 = seq.q0, n = seq.n, len = seq.len;
-  if ((long)n * a.group <= a.few_rows) return;
-  const long unit = (long)blockIdx.x * 4 + warp;
-  const int i = (int)(unit / a.h_q), h = (int)(unit % a.h_q), g = h / a.group;
-  if (i >= n) return;
-  const int p = len - n + i;
-  const T* qr = static_cast<const T*>(a.q) + (q0 + i) * a.q_row + h * a.q_head;
-  for (int e = lane; e < D; e += 32) qs[warp][e] = Elem<T>::to_float(qr[e]) * a.scale_log2;
-  __syncwarp();
-  float mx = -INFINITY, sum = 0.f, acc[E] = {};
-  const int lo = a.window ? max(0, p - a.window + 1) : 0;
-  const int n_sink = min(a.sinks, lo);
-  const int total = p < 0 ? 0 : n_sink + (p + 1 - lo);
-  for (int c0 = 0; c0 < total; c0 += 32) {
-    const int idx = c0 + lane;
-    const int j = idx < n_sink ? idx : idx - n_sink + lo;
-    float x = -INFINITY;
-    long tile_at = -1;
-    if (idx < total) {
-      const int page = a.pages[(long)b * a.max_pages + (j >> a.page_shift)];
-      if (page >= 0 && page < a.n_pages) {
-        const int in_page = j & ((1 << a.page_shift) - 1);
-        tile_at = (((long)page * a.h_kv + g << (a.page_shift - 4)) + (in_page >> 4)) * L::kBytes;
-        const uint8_t* tile = a.pool + tile_at;
-        const int t = j & 15;
-        x = 0.f;
-        for (int grp = 0; grp < L::G; grp++) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(tile + L::kKeyCodes + (grp * 16 + t) * 16);
-          const uint32_t z = *reinterpret_cast<const uint32_t*>(tile + L::kKeyGrid + (t * L::G + grp) * 4);
-          const float s = h2f((uint16_t)(z & 0xffff)), m = h2f((uint16_t)(z >> 16));
-          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-          for (int e = 0; e < 32; e++)
-            x = fmaf(qs[warp][grp * 32 + e], fmaf((float)((w[e >> 3] >> (4 * (e & 7))) & 15u), s, m), x);
-        }
-      } else {
-        kvp_note_bad(a.bad);
-      }
-    }
-    float top = x;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float now = fmaxf(mx, top);
-    if (now == -INFINITY) continue;  // the same in every lane
-    const float w = exp2f(x - now), old = exp2f(mx - now);
-    mx = now;
-    sum = sum * old + w;
-#pragma unroll
-    for (int e = 0; e < E; e++) acc[e] *= old;
-    for (int l = 0; l < 32; l++) {
-      const float wl = __shfl_sync(0xffffffffu, w, l);
-      const long at = __shfl_sync(0xffffffffu, tile_at, l);
-      const int t = __shfl_sync(0xffffffffu, j, l) & 15;
-      if (at < 0) continue;
-      const uint8_t* tile = a.pool + at;
-      const int e0 = lane * E, grp = e0 >> 5;
-      const uint16_t* vz =
-          reinterpret_cast<const uint16_t*>(tile + L::kValueGrid) + ((t >> 1) * L::G + grp) * 4 + (t & 1);
-      const float s = h2f(vz[0]), m = h2f(vz[2]);
-#pragma unroll
-      for (int e = 0; e < E; e++) {
-        const int d = (e0 + e) & 31;
-        const uint32_t c = (tile[L::kValueCodes + (grp * 16 + t) * 16 + (d >> 1)] >> (4 * (d & 1))) & 15u;
-        acc[e] = fmaf(wl, fmaf((float)c, s, m), acc[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  T* o = static_cast<T*>(a.out) + ((long)(q0 + i) * a.h_q + h) * D + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; e++) o[e] = Elem<T>::from_float(acc[e] * inv);
-}
-
-template <typename T, int D>
-sf_status launch_attend(const KvpAttendArgs& a, cudaStream_t s) {
-  const long units = (long)(a.cu_q ? a.n_q : a.n_q / a.batch) * a.h_q;
-  SF_CUDA(launch_pdl(kvp_attend_plain_kernel<T, D>, dim3((unsigned)((units + 3) / 4), 1, a.batch), dim3(128), 0, s, a));
-  return SF_OK;
-}
-
 sf_status check_attend(const sf_kvp* kv, int n_q, int batch, int h_q) {
   const sf_status st = check_kvp(kv);
   if (st != SF_OK) return st;
@@ -129,7 +35,12 @@ using namespace sf;
 
 extern "C" size_t sf_kvp_attend_workspace_bytes(const sf_kvp* kv, int n_q, int batch, int h_q) {
   if (check_attend(kv, n_q, batch, h_q) != SF_OK || n_q == 0) return 0;
-  return kvp_decode_workspace(kv->d, few_rows(n_q, batch, h_q / kv->h_kv));
+  // the two kernels of a call run one after the other and share the space
+  const int group = h_q / kv->h_kv;
+  const size_t few = kvp_decode_workspace(kv->d, few_rows(n_q, batch, group));
+  if ((long long)n_q * group <= kFewRows) return few;
+  const size_t many = kvp_prefill_workspace(kv->d);
+  return few > many ? few : many;
 }
 
 extern "C" sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_row, int64_t q_head, sf_dtype dtype,
@@ -177,7 +88,5 @@ extern "C" sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_ro
     if (e != SF_OK) return e;
   }
   if (cu_q ? (long long)n_q * a.group <= kFewRows : each <= kFewRows) return SF_OK;
-  if (kv->d == 128)
-    return dtype == SF_F16 ? launch_attend<__half, 128>(a, s) : launch_attend<__nv_bfloat16, 128>(a, s);
-  return dtype == SF_F16 ? launch_attend<__half, 64>(a, s) : launch_attend<__nv_bfloat16, 64>(a, s);
+  return launch_kvp_prefill(a, kv->d, dtype, s);
 }

@@ -24,6 +24,10 @@ struct KvpAttendArgs {
 size_t kvp_decode_workspace(int d, int rows);
 sf_status launch_kvp_decode(const KvpAttendArgs& a, int d, sf_dtype dtype, int rows, cudaStream_t s);
 
+// Many-row kernel (kvp_prefill.cu).
+size_t kvp_prefill_workspace(int d);
+sf_status launch_kvp_prefill(const KvpAttendArgs& a, int d, sf_dtype dtype, cudaStream_t s);
+
 __device__ __forceinline__ void kvp_note_bad(int32_t* bad) {
   if (bad) atomicAdd(bad, 1);
 }
@@ -66,6 +70,130 @@ __device__ __forceinline__ KvpSpan kvp_span(const KvpAttendArgs& a, int p0, int 
   s.sink = min((min(a.sinks, lo) + 15) >> 4, s.first);
   s.tiles = p1 < 0 ? 0 : s.sink + (p1 >> 4) + 1 - s.first;
   return s;
+}
+
+// ---- the cut of the work ----------------------------------------------------
+//
+// An item is (sequence, tile of ROWS query rows, KV head); its work is counted
+// in steps of STEP cache tiles.  The items lie end to end (sequences, row tiles,
+// KV heads, in that order) and the line of steps is cut into equal ranges, one
+// per CTA, on the device: the host needs no length.  Parts of an item that
+// several CTAs share are joined by a merge kernel in the order of the CTAs.
+// FEW: the sequences of at most few_rows rows, else the others.
+template <int ROWS, int STEP, bool FEW>
+struct KvpItem {
+  int b, rt, g;
+  KvpSeq seq;
+  KvpSpan span;
+  int steps;
+
+  static __device__ __forceinline__ int row_tiles(const KvpAttendArgs& a, const KvpSeq& s) {
+    const long rows = (long)s.n * a.group;
+    return rows == 0 || (rows <= a.few_rows) != FEW ? 0 : (int)((rows + ROWS - 1) / ROWS);
+  }
+  static __device__ __forceinline__ KvpSpan span_of(const KvpAttendArgs& a, const KvpSeq& s, int rt) {
+    const int last = min((rt + 1) * ROWS, s.n * a.group) - 1;
+    return kvp_span(a, s.len - s.n + rt * ROWS / a.group, s.len - s.n + last / a.group);
+  }
+  static __device__ __forceinline__ int steps_of(const KvpSpan& s) { return max(1, (s.tiles + STEP - 1) / STEP); }
+  // Steps of one sequence, over its row tiles (not yet times the KV heads).
+  static __device__ __forceinline__ long seq_steps(const KvpAttendArgs& a, const KvpSeq& s) {
+    const int n = row_tiles(a, s);
+    long sum = 0;
+    for (int rt = 0; rt < n; rt++) sum += steps_of(span_of(a, s, rt));
+    return sum;
+  }
+  __device__ __forceinline__ void set(const KvpAttendArgs& a) {
+    span = span_of(a, seq, rt);
+    steps = steps_of(span);
+  }
+  __device__ __forceinline__ void next(const KvpAttendArgs& a) {
+    if (++g < a.h_kv) return;
+    g = 0;
+    if (++rt >= row_tiles(a, seq)) {
+      rt = 0;
+      do seq = kvp_seq(a, ++b);
+      while (row_tiles(a, seq) == 0);
+    }
+    set(a);
+  }
+};
+
+// This CTA's range [u0, u1) of the line (u0 == u1: nothing), and the item and
+// place `at` on the line where it starts.  All threads call it.
+struct KvpRange {
+  long u0, u1, at, total, ctas;
+};
+struct KvpRangeShared {
+  long scan[32];
+  long at;
+  int b, rt, g;
+};
+template <int THREADS, int ROWS, int STEP, bool FEW>
+__device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_steps, KvpRangeShared& sh,
+                                              KvpItem<ROWS, STEP, FEW>& it) {
+  using Item = KvpItem<ROWS, STEP, FEW>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long mine = 0;
+  const int per = (a.batch + THREADS - 1) / THREADS;
+  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
+  for (int b = b0; b < b1; b++) mine += Item::seq_steps(a, kvp_seq(a, b)) * a.h_kv;
+  long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
+  __syncthreads();
+  KvpRange r;
+  r.total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; w++) {
+    if (w < warp) upto += sh.scan[w];
+    r.total += sh.scan[w];
+  }
+  r.ctas = min((long)gridDim.x, (r.total + min_steps - 1) / min_steps);
+  r.u0 = r.u1 = 0;
+  if ((long)blockIdx.x >= r.ctas) return r;  // all threads alike
+  r.u0 = r.total * blockIdx.x / r.ctas, r.u1 = r.total * (blockIdx.x + 1) / r.ctas;
+  if (r.u0 >= upto - mine && r.u0 < upto) {  // one thread
+    long at = upto - mine;
+    bool found = false;
+    for (int b = b0; b < b1 && !found; b++) {
+      const KvpSeq s = kvp_seq(a, b);
+      const int n = Item::row_tiles(a, s);
+      for (int rt = 0; rt < n && !found; rt++) {
+        const int st = Item::steps_of(Item::span_of(a, s, rt));
+        if (r.u0 < at + (long)st * a.h_kv) {
+          sh.b = b, sh.rt = rt, sh.g = (int)((r.u0 - at) / st);
+          sh.at = at + (long)sh.g * st;
+          found = true;
+        } else {
+          at += (long)st * a.h_kv;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  it.b = sh.b, it.rt = sh.rt, it.g = sh.g;
+  it.seq = kvp_seq(a, it.b);
+  it.set(a);
+  r.at = sh.at;
+  return r;
+}
+
+// An item that several CTAs share, written by the one with its start.
+struct KvpShared {
+  int q_row, row0, rows, head0;  // first query row of the sequence, first row, rows, first query head
+  int parts, pad[3];
+};
+// How many CTAs share the item [at, at + steps) that starts in this one's range.
+__device__ __forceinline__ int kvp_sharers(const KvpRange& r, long end) {
+  long last = (end * r.ctas + r.total - 1) / r.total - 1;
+  while (r.total * (last + 1) / r.ctas < end) last++;
+  while (r.total * last / r.ctas >= end) last--;
+  return (int)(last - blockIdx.x + 1);
 }
 
 __device__ __forceinline__ bool kvp_sees(const KvpAttendArgs& a, int p, int j) {

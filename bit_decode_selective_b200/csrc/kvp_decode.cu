@@ -23,10 +23,7 @@
 //     weights from S^T's layout to the operand's.
 //   - The running maximum moves only when some logit passes it by 2^6: then the
 //     sums are rescaled, otherwise a step costs one vote.
-// Work is cut on the device: the call's (sequence, row tile, KV head) items in
-// steps of 32 tokens, laid end to end and cut into equal ranges, one per CTA;
-// an item cut in several ranges is joined by the merge kernel in a fixed order.
-// So ragged batches are balanced without the host knowing a length.
+// The work is cut into equal ranges on the device (kvp_attend.cuh).
 #include "kvp_attend.cuh"
 
 namespace sf {
@@ -54,15 +51,10 @@ struct Cfg {
   static constexpr int kPartFloats = kRows * D + 2 * kRows;
 };
 
-struct Desc {  // an item that several CTAs share, written by the one with its start
-  int q_row, row0, rows, head0;  // first query row of the sequence, first row, rows, first query head
-  int parts, pad[3];
-};
-
 struct DecodeArgs {
   KvpAttendArgs a;
-  float* parts;  // [2 * ctas][part floats]
-  Desc* desc;    // [ctas]
+  float* parts;     // [2 * ctas][part floats]
+  KvpShared* desc;  // [ctas]
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -109,55 +101,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
-// ---- the cut of the work ----------------------------------------------------
-
-struct Item {  // (sequence, row tile, KV head) and its place in the line of steps
-  int b, rt, g;
-  KvpSeq seq;
-  KvpSpan span;
-  int steps;
-};
-
-template <int NT>
-__device__ __forceinline__ int row_tiles(const KvpAttendArgs& a, const KvpSeq& s) {
-  const long rows = (long)s.n * a.group;
-  return rows == 0 || rows > a.few_rows ? 0 : (int)((rows + 8 * NT - 1) / (8 * NT));
-}
-template <int NT>
-__device__ __forceinline__ KvpSpan item_span(const KvpAttendArgs& a, const KvpSeq& s, int rt) {
-  const int last = min((rt + 1) * 8 * NT, s.n * a.group) - 1;
-  const int base = s.len - s.n;
-  return kvp_span(a, base + rt * 8 * NT / a.group, base + last / a.group);
-}
-__device__ __forceinline__ int span_steps(const KvpSpan& s) { return max(1, (s.tiles + kStepTiles - 1) / kStepTiles); }
-
-// Steps of one sequence, over its row tiles (not yet times the KV heads).
-template <int NT>
-__device__ __forceinline__ long seq_steps(const KvpAttendArgs& a, const KvpSeq& s) {
-  const int n = row_tiles<NT>(a, s);
-  long sum = 0;
-  for (int rt = 0; rt < n; rt++) sum += span_steps(item_span<NT>(a, s, rt));
-  return sum;
-}
-
-template <int NT>
-__device__ __forceinline__ void set_item(const KvpAttendArgs& a, Item& it) {
-  it.span = item_span<NT>(a, it.seq, it.rt);
-  it.steps = span_steps(it.span);
-}
-// The item after `it`: the next KV head, row tile, or sequence with rows.
-template <int NT>
-__device__ __forceinline__ void next_item(const KvpAttendArgs& a, Item& it) {
-  if (++it.g < a.h_kv) return;
-  it.g = 0;
-  if (++it.rt >= row_tiles<NT>(a, it.seq)) {
-    it.rt = 0;
-    do it.seq = kvp_seq(a, ++it.b);
-    while (row_tiles<NT>(a, it.seq) == 0);
-  }
-  set_item<NT>(a, it);
-}
-
 // ---- the kernel -------------------------------------------------------------
 
 template <typename T, int D, int NT>
@@ -167,9 +110,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   constexpr int G = L::G, MT = D / 16;
   const KvpAttendArgs& a = da.a;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long scan[kWarps];
-  __shared__ long first_at;          // steps of the line before the first item
-  __shared__ int first_b, first_rt, first_g;
+  __shared__ KvpRangeShared range_sh;
   __shared__ int tile_base[kWarps][C::kStages][kStepTiles];  // first token of a staged tile, -1: none
   __shared__ float2 ml[kWarps][C::kRows];
   pdl_trigger();
@@ -177,55 +118,12 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, c = lane & 3;
 
-  // ---- this CTA's range [u0, u1) of the line of steps
-  long mine = 0;
-  const int per = (a.batch + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-  for (int b = b0; b < b1; b++) mine += seq_steps<NT>(a, kvp_seq(a, b)) * a.h_kv;
-  long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 31) scan[warp] = upto;
-  __syncthreads();
-  long total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; w++) {
-    if (w < warp) upto += scan[w];
-    total += scan[w];
-  }
-  // ranges of at least one step per warp
-  const long ctas = min((long)gridDim.x, (total + kWarps - 1) / kWarps);
+  KvpItem<C::kRows, kStepTiles, true> it;
+  const KvpRange range = kvp_range<kThreads>(a, kWarps, range_sh, it);  // at least a step per warp
   if (tid == 0) da.desc[blockIdx.x].parts = 0;
-  if ((long)blockIdx.x >= ctas) return;  // all threads alike
-  const long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
-  if (u0 >= upto - mine && u0 < upto) {  // one thread
-    long at = upto - mine;
-    for (int b = b0; b < b1; b++) {
-      const KvpSeq s = kvp_seq(a, b);
-      const int n = row_tiles<NT>(a, s);
-      bool found = false;
-      for (int rt = 0; rt < n && !found; rt++) {
-        const int st = span_steps(item_span<NT>(a, s, rt));
-        if (u0 < at + (long)st * a.h_kv) {
-          first_b = b, first_rt = rt, first_g = (int)((u0 - at) / st);
-          first_at = at + (long)first_g * st;
-          found = true;
-        } else {
-          at += (long)st * a.h_kv;
-        }
-      }
-      if (found) break;
-    }
-  }
-  __syncthreads();
-  Item it;
-  it.b = first_b, it.rt = first_rt, it.g = first_g;
-  it.seq = kvp_seq(a, it.b);
-  set_item<NT>(a, it);
-  long at = first_at;
+  if (range.u0 == range.u1) return;
+  const long u0 = range.u0, u1 = range.u1;
+  long at = range.at;
 
   uint8_t* stage0 = smem + warp * C::kWarpBytes;
   const uint32_t stage0_u = smem_u32(stage0);
@@ -613,21 +511,16 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
     }
     // the CTA with the item's start tells the merge kernel how many share it
     if (!all && s0 == 0 && tid == 0) {
-      // the last CTA whose range begins before the item's end
-      const long end = at + it.steps;
-      long last = (end * ctas + total - 1) / total - 1;
-      while (total * (last + 1) / ctas < end) last++;
-      while (total * last / ctas >= end) last--;
-      Desc d;
+      KvpShared d;
       d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
-      d.parts = (int)(last - blockIdx.x + 1);
+      d.parts = kvp_sharers(range, at + it.steps);
       d.pad[0] = d.pad[1] = d.pad[2] = 0;
       da.desc[blockIdx.x] = d;
     }
     __syncthreads();  // the exchange is read
     if (at + it.steps >= u1) break;
     at += it.steps;
-    next_item<NT>(a, it);
+    it.next(a);
   }
 }
 
@@ -644,7 +537,7 @@ __global__ void __launch_bounds__(kThreads) kvp_merge_kernel(const __grid_consta
   __shared__ float tops[kWarps];
   pdl_trigger();
   pdl_wait();
-  const Desc d = da.desc[blockIdx.x];
+  const KvpShared d = da.desc[blockIdx.x];
   const int r = blockIdx.y, tid = threadIdx.x;
   if (d.parts == 0 || r >= d.rows) return;
   auto part = [&](int i) {  // the first lies in the starting CTA's second place, the others in their CTA's first
@@ -699,7 +592,7 @@ sf_status launch_decode(const KvpAttendArgs& a, cudaStream_t s) {
   const int ctas = decode_ctas(NT);
   DecodeArgs da;
   da.a = a;
-  da.desc = static_cast<Desc*>(a.ws);
+  da.desc = static_cast<KvpShared*>(a.ws);
   da.parts = reinterpret_cast<float*>(da.desc + ctas);
   SF_CUDA(cudaFuncSetAttribute(kvp_decode_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
   SF_CUDA(launch_pdl(kvp_decode_kernel<T, D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, s, da));
@@ -720,7 +613,7 @@ sf_status launch_decode_nt(const KvpAttendArgs& a, int rows, cudaStream_t s) {
 
 size_t kvp_decode_workspace(int d, int rows) {
   const int nt = row_blocks(rows), ctas = decode_ctas(nt);
-  return (size_t)ctas * (sizeof(Desc) + 2 * (8 * nt * d + 16 * nt) * sizeof(float));
+  return (size_t)ctas * (sizeof(KvpShared) + 2 * (8 * nt * d + 16 * nt) * sizeof(float));
 }
 
 sf_status launch_kvp_decode(const KvpAttendArgs& a, int d, sf_dtype dtype, int rows, cudaStream_t s) {

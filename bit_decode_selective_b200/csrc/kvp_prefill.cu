@@ -1,0 +1,643 @@
+// kvp_prefill.cu -- attention over the paged 4-bit cache for sequences with
+// many query rows (prefill, prefill chunks behind a cached prefix).
+//
+// 4 d products per (row, token) against 1.25 d bytes per token make this a
+// matrix problem: tcgen05 products of 128-row tiles with fp32 accumulators in
+// TMEM.  Rows are query tokens x the query heads of one KV head, so that heads
+// that share keys and values share their decoding.  A CTA takes 256 rows as two
+// tiles and walks the visible cache 128 tokens at a time:
+//   warps 0-3, 4-7  softmax of tile 0, 1: a thread owns a row.  S comes out of
+//                   TMEM, the weights go back into S's columns as the fp16
+//                   operand of the second product.  While one tile's weights
+//                   are made the tensor core works for the other.
+//   warps 8-11      decode 128 tokens' codes to fp16 keys and values in shared
+//                   memory (128-byte swizzle), once for both tiles
+//   warp 12         one thread issues the products
+// Numerics: keys and values are rounded once to fp16, as a 16-bit cache would
+// hold them; queries are scaled per row by a power of two into fp16's range
+// (exact for fp16 and bf16 but for elements 2^24 below the row's largest);
+// weights are rounded to fp16, scaled so that the largest is near 2^15; sums are
+// fp32.  The softmax reference moves only when a logit passes it by 2^6, so the
+// output sums are hardly ever rescaled.
+//
+// Elements of 8 are kept in the order (0 4 1 5 2 6 3 7), the order in which a
+// masked code word gives them up: queries and keys alike, and the output's
+// columns are put back in order when they are stored.
+//
+// The work is cut into equal ranges on the device (kvp_attend.cuh); every wait
+// is bounded.
+#include "internal.cuh"
+#include "kvp_attend.cuh"
+
+namespace sf {
+namespace {
+
+constexpr int kRows = 256, kTileRows = 128;
+constexpr int kStep = 8;                 // cache tiles per step: 128 tokens
+constexpr int kTokens = kStep * kKvpTile;
+constexpr int kSoftWarps = 8, kFillWarps = 4;
+constexpr int kThreads = (kSoftWarps + kFillWarps + 4) * 32;  // the last warpgroup issues the products
+// registers per thread of the three kinds of warpgroup; together the 128 x 512
+// of the launch (65,536): 2 x 184 + 96 + 48 = 4 x 128
+constexpr int kSoftRegs = 184, kFillRegs = 96, kIssueRegs = 48;
+constexpr int kRing = 4;                 // steps whose token places are kept
+constexpr float kRefGap = 6.f, kRefShift = 9.f;
+constexpr unsigned long long kWaitNs = 1000000000ull;  // bounded waits give up after 1 s
+constexpr int kMinSteps = 1;
+
+__device__ unsigned int g_wait_timeouts;
+
+using Item = KvpItem<kRows, kStep, false>;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;              // 64-element halves of a 128-byte swizzled row
+  static constexpr int kTileBytes = kHalves * 16384;  // 128 rows
+  static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = 4 * kTileBytes;
+  static constexpr int kSmem = 6 * kTileBytes + 1024;  // + alignment
+  static constexpr int kPartFloats = kRows * D + 2 * kRows;
+};
+
+struct PrefillArgs {
+  KvpAttendArgs a;
+  float* parts;     // [2 * ctas][part floats]
+  KvpShared* desc;  // [ctas]
+};
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- PTX --------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase for at most kWaitNs; after one wait of the CTA has given
+// up none waits any more, and the CTA runs to its end without a result.
+__device__ __forceinline__ void mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try(bar, parity)) {
+    if (*gave_up) return;
+    if (now_ns() - t0 > kWaitNs) {
+      *gave_up = 1;
+      atomicAdd(&g_wait_timeouts, 1u);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+  if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, gave_up);
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// Descriptor of a 128-byte swizzled operand.  Contraction along the rows'
+// bytes (queries, keys): `far` unused, 8-row groups 1024 bytes apart.
+// Contraction along the rows (values): 64-element halves `far` bytes apart,
+// 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t far) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(far >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t mma_desc(int n, bool b_by_rows) {  // fp16 x fp16 -> fp32, M = 128
+  return (1u << 4) | (b_by_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// 8 codes of a word to fp16 values in the order (0 4)(1 5)(2 6)(3 7): 1024 +
+// code by masking into the mantissa, minus 1024, times s, plus m.
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, __half2 m) {
+  const __half2 one16 = __float2half2_rn(0.0625f), off1 = __float2half2_rn(-1024.f), off16 = __float2half2_rn(-64.f);
+  const uint32_t v = w >> 8;
+  uint4 r;
+  r.x = as_u32(__hfma2(__hadd2(as_h2((w & 0x000F000Fu) | 0x64006400u), off1), s, m));
+  r.y = as_u32(__hfma2(__hfma2(as_h2((w & 0x00F000F0u) | 0x64006400u), one16, off16), s, m));
+  r.z = as_u32(__hfma2(__hadd2(as_h2((v & 0x000F000Fu) | 0x64006400u), off1), s, m));
+  r.w = as_u32(__hfma2(__hfma2(as_h2((v & 0x00F000F0u) | 0x64006400u), one16, off16), s, m));
+  return r;
+}
+
+struct Control {
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], last;
+  KvpRangeShared range;
+  // first token of each cache tile of the step, low bit: all rows see all of
+  // it; -16: nothing there
+  int place[kRing][kStep];
+  uint32_t tmem;
+  volatile int gave_up;
+};
+
+// Bit i: the row at position p sees token base + i (16 tokens).
+__device__ __forceinline__ uint32_t seen16(const KvpAttendArgs& a, int p, int base) {
+  if (base < 0) return 0;
+  const auto below = [](int n) { return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u; };  // bits 0 .. n-1
+  uint32_t m = below(p - base + 1);
+  if (a.window) m &= ~below(p - a.window + 1 - base) | below(a.sinks - base);
+  return m;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_constant__ PrefillArgs pa) {
+  using L = KvpTile<D>;
+  using C = Cfg<D>;
+  constexpr int G = L::G;
+  const KvpAttendArgs& a = pa.a;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Control ctl;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t smem_at = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  if (tid == 0) {
+    for (int t = 0; t < 2; t++) {
+      mbar_init(&ctl.q_full[t], kTileRows), mbar_init(&ctl.s_full[t], 1);
+      mbar_init(&ctl.p_full[t], kTileRows), mbar_init(&ctl.o_done[t], 1);
+      mbar_init(&ctl.k_full[t], kFillWarps * 32), mbar_init(&ctl.k_empty[t], 1);
+      mbar_init(&ctl.v_full[t], kFillWarps * 32), mbar_init(&ctl.v_empty[t], 1);
+    }
+    mbar_init(&ctl.last, 1);
+    ctl.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+  Item it;
+  const KvpRange range = kvp_range<kThreads>(a, kMinSteps, ctl.range, it);
+  if (tid == 0) pa.desc[blockIdx.x].parts = 0;
+  if (range.u0 == range.u1) return;
+  if (warp == kSoftWarps + kFillWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = ctl.tmem;  // columns: S tile 0, S tile 1 (128 each), O tile 0, O tile 1 (D each)
+  long at = range.at;
+  int step_no = 0;  // steps of this CTA so far, over all segments
+
+  if (warp < kSoftWarps) {
+    regs_up<kSoftRegs>();
+    // ======================= softmax: a row per thread ========================
+    const int t = warp >> 2, tr = tid & 127, r = t * kTileRows + tr;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp & 3)
+    const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
+    int n_s = 0, n_o = 0;  // phases of s_full, o_done
+    for (;;) {
+      const int s0 = (int)(max(range.u0, at) - at), s1 = (int)(min(range.u1, at + it.steps) - at);
+      const int row0 = it.rt * kRows, rows = min(it.seq.n * a.group - row0, kRows);
+      if (t == 0 || rows > kTileRows) {
+        const int rr = row0 + min(r, rows - 1);
+        const int qi = it.seq.q0 + rr / a.group, head = it.g * a.group + rr % a.group;
+        const int pos = it.seq.len - it.seq.n + rr / a.group;
+        // ---- the row's query, scaled into fp16's range
+        const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qi * a.q_row + head * a.q_head);
+        float top = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; i++) {
+          const uint4 w = qr[i];
+          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const float2 f = Elem<T>::to_float2(ws[e]);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 100);
+        const float up = r < rows ? __uint_as_float((uint32_t)(127 + 10 - e) << 23) : 0.f;
+        const float kappa = __uint_as_float((uint32_t)(127 - 10 + e) << 23) * a.scale_log2;
+#pragma unroll 4
+        for (int i = 0; i < D / 8; i++) {
+          const uint4 w = qr[i];
+          const float2 f0 = Elem<T>::to_float2(w.x), f1 = Elem<T>::to_float2(w.y);
+          const float2 f2 = Elem<T>::to_float2(w.z), f3 = Elem<T>::to_float2(w.w);
+          uint4 o;
+          o.x = pack2(f0.x * up, f2.x * up), o.y = pack2(f0.y * up, f2.y * up);
+          o.z = pack2(f1.x * up, f3.x * up), o.w = pack2(f1.y * up, f3.y * up);
+          *reinterpret_cast<uint4*>(smem + C::kQ + t * C::kTileBytes + (i >> 3) * 16384 + tr * 128 +
+                                    (((i & 7) ^ (tr & 7)) << 4)) = o;
+        }
+        fence_async_smem();
+        tc_before();
+        mbar_arrive(&ctl.q_full[t]);
+
+        float ref = -INFINITY, l = 0.f;
+        for (int j = s0; j < s1; j++) {
+          mbar_wait(&ctl.s_full[t], n_s & 1, &ctl.gave_up);
+          n_s++;
+          tc_after();
+          const int ring = (step_no + j - s0) & (kRing - 1);
+          const int4 pl0 = *reinterpret_cast<const int4*>(&ctl.place[ring][0]);
+          const int4 pl1 = *reinterpret_cast<const int4*>(&ctl.place[ring][4]);
+          const int place[kStep] = {pl0.x, pl0.y, pl0.z, pl0.w, pl1.x, pl1.y, pl1.z, pl1.w};
+          const bool whole = (place[0] & place[1] & place[2] & place[3] & place[4] & place[5] & place[6] & place[7]) & 1;
+          uint32_t p[kTokens / 2];
+          float sum;
+          for (;;) {
+            // weights against the present reference; done again when a logit passes it too far
+            const float off = (ref == -INFINITY ? 0.f : ref) - kRefShift;
+            float ymax = -INFINITY;
+            sum = 0.f;
+#pragma unroll
+            for (int ch = 0; ch < kTokens / 32; ch++) {
+              uint32_t s[32];
+              tc_ld32(s, s_at + ch * 32);
+              tc_wait_ld();
+              float y[32];
+#pragma unroll
+              for (int i = 0; i < 32; i++) y[i] = fmaf(__uint_as_float(s[i]), kappa, -off);
+              if (!whole) {
+                const uint32_t seen = seen16(a, pos, place[2 * ch] & ~1) | (seen16(a, pos, place[2 * ch + 1] & ~1) << 16);
+#pragma unroll
+                for (int i = 0; i < 32; i++) y[i] = seen >> i & 1 ? y[i] : -INFINITY;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                ymax = fmaxf(ymax, fmaxf(y[i], y[i + 1]));
+                const float p0 = ex2(y[i]), p1 = ex2(y[i + 1]);
+                sum += p0 + p1;
+                p[ch * 16 + i / 2] = pack2(p0, p1);
+              }
+            }
+            const float top2 = ymax + off;
+            if (!__any_sync(0xffffffffu, top2 > ref + kRefGap)) break;
+            const float next = fmaxf(ref, top2);
+            const float f = next == -INFINITY ? 1.f : ex2(ref - next);
+            ref = next;
+            l *= f;
+            if (j > s0) {  // the products into O so far are complete: S was issued after them
+#pragma unroll
+              for (int ch = 0; ch < D / 32; ch++) {
+                uint32_t o[32];
+                tc_ld32(o, o_at + ch * 32);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tc_st32(o_at + ch * 32, o);
+              }
+              tc_wait_st();
+            }
+          }
+          l += sum;
+          tc_st32(s_at, p);
+          tc_st32(s_at + 32, p + 32);
+          tc_wait_st();
+          tc_before();
+          mbar_arrive(&ctl.p_full[t]);
+        }
+
+        // ---- the row's output, or its part of it
+        mbar_wait(&ctl.o_done[t], n_o & 1, &ctl.gave_up);
+        n_o++;
+        tc_after();
+        const bool all = s0 == 0 && s1 == it.steps;
+        float* part = pa.parts + (size_t)(2 * blockIdx.x + (range.u0 > at ? 0 : 1)) * C::kPartFloats;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
+        T* out = static_cast<T*>(a.out) + ((size_t)qi * a.h_q + head) * D;
+#pragma unroll
+        for (int ch = 0; ch < D / 32; ch++) {
+          uint32_t o[32];
+          tc_ld32(o, o_at + ch * 32);
+          tc_wait_ld();
+          if (r < rows) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 4; i++) v[i] = __uint_as_float(o[k + 2 * i]), v[i + 4] = __uint_as_float(o[k + 2 * i + 1]);
+              if (all) {
+                uint4 w;
+                w.x = Elem<T>::from_float2(v[0] * inv, v[1] * inv), w.y = Elem<T>::from_float2(v[2] * inv, v[3] * inv);
+                w.z = Elem<T>::from_float2(v[4] * inv, v[5] * inv), w.w = Elem<T>::from_float2(v[6] * inv, v[7] * inv);
+                *reinterpret_cast<uint4*>(out + ch * 32 + k) = w;
+              } else {
+                float4* w = reinterpret_cast<float4*>(part + r * D + ch * 32 + k);
+                w[0] = make_float4(v[0], v[1], v[2], v[3]);
+                w[1] = make_float4(v[4], v[5], v[6], v[7]);
+              }
+            }
+          }
+        }
+        if (!all && r < rows) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(ref, l);
+        if (!all && s0 == 0 && tid == 0) {
+          KvpShared d;
+          d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
+          d.parts = kvp_sharers(range, at + it.steps);
+          d.pad[0] = d.pad[1] = d.pad[2] = 0;
+          pa.desc[blockIdx.x] = d;
+        }
+      }
+      step_no += s1 - s0;
+      if (at + it.steps >= range.u1) break;
+      at += it.steps;
+      it.next(a);
+    }
+  } else if (warp < kSoftWarps + kFillWarps) {
+    regs_down<kFillRegs>();
+    // ======================= decoding: a token per thread =====================
+    const int fw = warp - kSoftWarps, tk = fw * 32 + lane, sub = tk >> 4, tt = tk & 15;
+    uint4 kc[G], vc[G], kz, vz[G / 2];
+    for (;;) {
+      const int s0 = (int)(max(range.u0, at) - at), s1 = (int)(min(range.u1, at + it.steps) - at);
+      const int32_t* pages = a.pages + (long)it.b * a.max_pages;
+      // the page entry of this thread's cache tile of a step (-1: none), and the tile's address
+      auto entry = [&](int step) {
+        const int i = step * kStep + sub;
+        if (step >= s1 || i >= it.span.tiles) return -1;
+        const int page = pages[it.span.tile(i) >> (a.page_shift - 4)];
+        if (page >= 0 && page < a.n_pages) return page;
+        if (tt == 0) kvp_note_bad(a.bad);
+        return -1;
+      };
+      auto tile_of = [&](int page, int step) -> const uint8_t* {
+        if (page < 0) return nullptr;
+        const int in_page = it.span.tile(step * kStep + sub) & ((1 << (a.page_shift - 4)) - 1);
+        return a.pool + ((((size_t)page * a.h_kv + it.g) << (a.page_shift - 4)) + in_page) * L::kBytes;
+      };
+      auto load_k = [&](const uint8_t* p) {
+#pragma unroll
+        for (int g = 0; g < G; g++)
+          kc[g] = p ? __ldg(reinterpret_cast<const uint4*>(p + L::kKeyCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
+        kz = make_uint4(0, 0, 0, 0);
+        if (p) {
+          if constexpr (G == 4) {
+            kz = __ldg(reinterpret_cast<const uint4*>(p + L::kKeyGrid + tt * 16));
+          } else {
+            const uint2 z = __ldg(reinterpret_cast<const uint2*>(p + L::kKeyGrid + tt * 8));
+            kz.x = z.x, kz.y = z.y;
+          }
+        }
+      };
+      auto load_v = [&](const uint8_t* p) {
+#pragma unroll
+        for (int g = 0; g < G; g++)
+          vc[g] = p ? __ldg(reinterpret_cast<const uint4*>(p + L::kValueCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int g = 0; g < G / 2; g++)
+          vz[g] = p ? __ldg(reinterpret_cast<const uint4*>(p + L::kValueGrid + (tt >> 1) * (8 * G) + g * 16))
+                    : make_uint4(0, 0, 0, 0);
+      };
+      auto put = [&](uint8_t* dst, int g, const uint4& codes, __half2 s, __half2 m) {
+        const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          *reinterpret_cast<uint4*>(dst + (g >> 1) * 16384 + tk * 128 + ((((g & 1) * 4 + i) ^ (tk & 7)) << 4)) =
+              decode8(w[i], s, m);
+      };
+      int page = entry(s0), page_next = entry(s0 + 1);
+      const uint8_t* tile = tile_of(page, s0);
+      load_k(tile);
+      load_v(tile);
+      for (int j = s0; j < s1; j++) {
+        const int no = step_no + j - s0, st = no & 1;
+        const uint32_t empty = ((no >> 1) & 1) ^ 1;
+        const int first = tile ? it.span.tile(j * kStep + sub) * 16 : -16;
+        const bool sees = tile && kvp_sees_all(a, it.span.p0, it.span.p1, first, 16);
+        // a token that no row sees may hold anything: it counts as zeros
+        const bool live = sees || (tile && kvp_some_sees(a, it.span.p0, it.span.p1, first + tt));
+        const uint8_t* next = tile_of(page_next, j + 1);
+        page_next = entry(j + 2);
+        mbar_wait(&ctl.k_empty[st], empty, &ctl.gave_up);
+        if (tt == 0) ctl.place[no & (kRing - 1)][sub] = first | (sees ? 1 : 0);
+        {
+          const uint32_t z[4] = {kz.x, kz.y, kz.z, kz.w};
+#pragma unroll
+          for (int g = 0; g < G; g++) {
+            const __half2 sm = as_h2(live ? z[g] : 0u);
+            put(smem + C::kK + st * C::kTileBytes, g, kc[g], __low2half2(sm), __high2half2(sm));
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(&ctl.k_full[st]);
+        load_k(next);
+        mbar_wait(&ctl.v_empty[st], empty, &ctl.gave_up);
+        {
+          const uint32_t z[8] = {vz[0].x, vz[0].y, vz[0].z, vz[0].w, vz[G / 2 - 1].x, vz[G / 2 - 1].y, vz[G / 2 - 1].z, vz[G / 2 - 1].w};
+#pragma unroll
+          for (int g = 0; g < G; g++) {
+            const __half2 ss = as_h2(live ? z[2 * g] : 0u), mm = as_h2(live ? z[2 * g + 1] : 0u);
+            put(smem + C::kV + st * C::kTileBytes, g, vc[g], tt & 1 ? __high2half2(ss) : __low2half2(ss),
+                tt & 1 ? __high2half2(mm) : __low2half2(mm));
+          }
+        }
+        fence_async_smem();
+        mbar_arrive(&ctl.v_full[st]);
+        load_v(next);
+        tile = next;
+      }
+      step_no += s1 - s0;
+      if (at + it.steps >= range.u1) break;
+      at += it.steps;
+      it.next(a);
+    }
+  } else {
+    regs_down<kIssueRegs>();
+    // ======================= the products =====================================
+    if (warp == kSoftWarps + kFillWarps && lane == 0) {
+      constexpr uint32_t kS = mma_desc(kTokens, false), kO = mma_desc(D, true);
+      int n_q[2] = {0, 0}, n_p[2] = {0, 0};  // phases of q_full, p_full
+      for (;;) {
+        const int s0 = (int)(max(range.u0, at) - at), s1 = (int)(min(range.u1, at + it.steps) - at);
+        const int tiles = it.seq.n * a.group - it.rt * kRows > kTileRows ? 2 : 1;
+        for (int j = s0; j <= s1; j++) {
+          const int no = step_no + j - s0, st = no & 1;
+          if (j < s1) mbar_wait(&ctl.k_full[st], (no >> 1) & 1, &ctl.gave_up);
+          for (int t = 0; t < tiles; t++) {
+            if (j > s0) {  // O += P V of the step before
+              const int b = no - 1, bst = b & 1;
+              if (t == 0) mbar_wait(&ctl.v_full[bst], (b >> 1) & 1, &ctl.gave_up);
+              mbar_wait(&ctl.p_full[t], n_p[t]++ & 1, &ctl.gave_up);
+              tc_after();
+              const uint32_t v_at = smem_at + C::kV + bst * C::kTileBytes;
+  #pragma unroll
+              for (int ks = 0; ks < kTokens / 16; ks++)
+                tc_mma_ts(tmem + 256 + t * D, tmem + t * 128 + ks * 8, smem_desc(v_at + ks * 2048, 16384), kO,
+                          j - 1 > s0 || ks > 0);
+              if (t == tiles - 1) tc_commit(&ctl.v_empty[bst]);
+              if (j == s1) tc_commit(&ctl.o_done[t]);
+            }
+            if (j < s1) {  // S = Q K
+              if (j == s0) {
+                mbar_wait(&ctl.q_full[t], n_q[t]++ & 1, &ctl.gave_up);
+                tc_after();
+              }
+              const uint32_t q_at = smem_at + C::kQ + t * C::kTileBytes, k_at = smem_at + C::kK + st * C::kTileBytes;
+  #pragma unroll
+              for (int ks = 0; ks < D / 16; ks++) {
+                const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                tc_mma_ss(tmem + t * 128, smem_desc(q_at + off, 16), smem_desc(k_at + off, 16), kS, ks > 0);
+              }
+              tc_commit(&ctl.s_full[t]);
+              if (t == tiles - 1) tc_commit(&ctl.k_empty[st]);
+            }
+          }
+        }
+        step_no += s1 - s0;
+        if (at + it.steps >= range.u1) break;
+        at += it.steps;
+        it.next(a);
+      }
+      tc_commit(&ctl.last);  // nothing is in flight when TMEM is given back
+      for (unsigned long long t0 = now_ns(); !mbar_try(&ctl.last, 0) && now_ns() - t0 < kWaitNs;) {
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == kSoftWarps + kFillWarps) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// One CTA per (CTA of the pass, 4 or 8 rows): joins the parts of the item that
+// starts there, in the order of the CTAs; 4 elements per thread.
+constexpr int kMergeThreads = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) kvp_prefill_merge_kernel(const __grid_constant__ PrefillArgs pa) {
+  using C = Cfg<D>;
+  constexpr int kPer = kMergeThreads / (D / 4);
+  const KvpAttendArgs& a = pa.a;
+  pdl_trigger();
+  pdl_wait();
+  const KvpShared d = pa.desc[blockIdx.x];
+  const int r = blockIdx.y * kPer + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4) * 4;
+  if (d.parts == 0 || r >= d.rows) return;
+  auto part = [&](int i) {  // the first lies in the starting CTA's second place, the others in their CTA's first
+    return pa.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::kPartFloats;
+  };
+  float top = -INFINITY;
+  for (int i = 0; i < d.parts; i++) top = fmaxf(top, part(i)[kRows * D + 2 * r]);
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < d.parts; i++) {
+    const float* p = part(i);
+    const float2 m = *reinterpret_cast<const float2*>(p + kRows * D + 2 * r);
+    const float4 v = *reinterpret_cast<const float4*>(p + r * D + d4);
+    const float f = m.x == -INFINITY ? 0.f : ex2(m.x - top);
+    sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+    sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+    l = fmaf(f, m.y, l);
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int qi = d.q_row + (d.row0 + r) / a.group, h = d.head0 + (d.row0 + r) % a.group;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((size_t)qi * a.h_q + h) * D + d4) =
+      make_uint2(Elem<T>::from_float2(sum.x * inv, sum.y * inv), Elem<T>::from_float2(sum.z * inv, sum.w * inv));
+}
+
+template <typename T, int D>
+sf_status launch_prefill(const KvpAttendArgs& a, cudaStream_t s) {
+  using C = Cfg<D>;
+  const int ctas = num_sms();
+  PrefillArgs pa;
+  pa.a = a;
+  pa.desc = static_cast<KvpShared*>(a.ws);
+  pa.parts = reinterpret_cast<float*>(pa.desc + ctas);
+  SF_CUDA(cudaFuncSetAttribute(kvp_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  SF_CUDA(launch_pdl(kvp_prefill_kernel<T, D>, dim3(ctas), dim3(kThreads), C::kSmem, s, pa));
+  SF_CUDA(launch_pdl(kvp_prefill_merge_kernel<T, D>, dim3(ctas, kRows / (kMergeThreads / (D / 4))), dim3(kMergeThreads),
+                     0, s, pa));
+  return SF_OK;
+}
+
+}  // namespace
+
+size_t kvp_prefill_workspace(int d) {
+  return (size_t)num_sms() * (sizeof(KvpShared) + 2 * (kRows * d + 2 * kRows) * sizeof(float));
+}
+
+sf_status launch_kvp_prefill(const KvpAttendArgs& a, int d, sf_dtype dtype, cudaStream_t s) {
+  if (d == 128) return dtype == SF_F16 ? launch_prefill<__half, 128>(a, s) : launch_prefill<__nv_bfloat16, 128>(a, s);
+  return dtype == SF_F16 ? launch_prefill<__half, 64>(a, s) : launch_prefill<__nv_bfloat16, 64>(a, s);
+}
+
+cudaError_t kvp_wait_timeouts(unsigned int* count, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned int));
+  if (e == cudaSuccess && reset) {
+    const unsigned int zero = 0;
+    e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(unsigned int));
+  }
+  return e;
+}
+
+}  // namespace sf

@@ -221,7 +221,8 @@ SF_API sf_status sf_gemv_refined_split(const sf_wq* w, const uint16_t* x, int ba
                                 float* y_corr, sf_stream_t stream);
 
 /* Number of bounded device-side waits that ran out on the current device
- * (*count), optionally reset to 0 (reset != 0).  The refined GEMV waits on
+ * (*count), optionally reset to 0 (reset != 0).  The refined GEMV and the paged
+ * cache's attention wait on
  * shared-memory barriers for its bulk copies; each such wait gives up after one
  * second, counts itself here and lets the kernel finish without its result
  * (the output is then undefined), so a fault in the memory system shows up as
