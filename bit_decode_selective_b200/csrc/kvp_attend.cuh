@@ -2,6 +2,8 @@
 // the call's arguments, a sequence's bounds and the tiles its queries see.
 #pragma once
 
+#include <atomic>
+
 #include "kvp.cuh"
 
 namespace sf {
@@ -19,6 +21,18 @@ struct KvpAttendArgs {
   int few_rows;                               // sequences of at most this many rows are the few-row kernel's
   void* ws;
 };
+
+// Raises a kernel's dynamic shared memory limit, once per device.
+template <auto kernel>
+inline cudaError_t kvp_allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return e;
+}
 
 // Few-row kernel (kvp_decode.cu): rows = queries x group of one sequence and KV head.
 size_t kvp_decode_workspace(int d, int rows);

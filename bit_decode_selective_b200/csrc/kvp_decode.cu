@@ -24,6 +24,8 @@
 //   - The running maximum moves only when some logit passes it by 2^6: then the
 //     sums are rescaled, otherwise a step costs one vote.
 // The work is cut into equal ranges on the device (kvp_attend.cuh).
+#include <algorithm>
+
 #include "kvp_attend.cuh"
 
 namespace sf {
@@ -524,57 +526,63 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   }
 }
 
-// One CTA per (CTA of the pass, row): joins the parts of the item that starts
-// there and goes on into the ranges of the CTAs after it.  A thread sums 4
-// elements over every (128 / (D / 4))-th part; the shares are then added in order.
+// One CTA per (CTA of the pass, 4 rows): joins the parts of the item that
+// starts there and goes on into the ranges of the CTAs after it.  128 threads a
+// row: a thread sums 4 elements over every (512 / D)-th part, and the shares
+// are added in order.
+constexpr int kMergeRows = 4, kMergeThreads = 128 * kMergeRows;
+
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads) kvp_merge_kernel(const __grid_constant__ DecodeArgs da) {
+__global__ void __launch_bounds__(kMergeThreads) kvp_merge_kernel(const __grid_constant__ DecodeArgs da) {
   using C = Cfg<D, NT>;
-  constexpr int kShares = kThreads / (D / 4);
+  constexpr int kShares = 128 / (D / 4);
   const KvpAttendArgs& a = da.a;
-  __shared__ float4 sums[kShares][D / 4];
-  __shared__ float ls[kShares];
-  __shared__ float tops[kWarps];
+  __shared__ float4 sums[kMergeRows][kShares][D / 4];
+  __shared__ float ls[kMergeRows][kShares], tops[kMergeRows][4];
   pdl_trigger();
   pdl_wait();
   const KvpShared d = da.desc[blockIdx.x];
-  const int r = blockIdx.y, tid = threadIdx.x;
-  if (d.parts == 0 || r >= d.rows) return;
+  const int rt = threadIdx.x >> 7, r = blockIdx.y * kMergeRows + rt, tid = threadIdx.x & 127;
+  if (d.parts == 0) return;
+  const bool live = r < d.rows;
   auto part = [&](int i) {  // the first lies in the starting CTA's second place, the others in their CTA's first
     return da.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::kPartFloats;
   };
   float top = -INFINITY;
-  for (int i = tid; i < d.parts; i += kThreads) top = fmaxf(top, part(i)[C::kRows * D + 2 * r]);
+  if (live)
+    for (int i = tid; i < d.parts; i += 128) top = fmaxf(top, part(i)[C::kRows * D + 2 * r]);
 #pragma unroll
   for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-  if ((tid & 31) == 0) tops[tid >> 5] = top;
+  if ((tid & 31) == 0) tops[rt][tid >> 5] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  top = fmaxf(fmaxf(tops[rt][0], tops[rt][1]), fmaxf(tops[rt][2], tops[rt][3]));
   const int share = tid / (D / 4), q4 = tid % (D / 4);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
+  if (live) {
 #pragma unroll 4
-  for (int i = share; i < d.parts; i += kShares) {
-    const float* p = part(i);
-    const float2 m = *reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r);
-    const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * q4);
-    const float f = m.x == -INFINITY ? 0.f : ex2(m.x - top);
-    sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
-    sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
-    l = fmaf(f, m.y, l);
-  }
-  sums[share][q4] = sum;
-  if (q4 == 0) ls[share] = l;
-  __syncthreads();
-  if (share == 0) {
-#pragma unroll
-    for (int k = 1; k < kShares; k++) {
-      const float4 v = sums[k][q4];
-      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    for (int i = share; i < d.parts; i += kShares) {
+      const float* p = part(i);
+      const float2 m = *reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r);
+      const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * q4);
+      const float f = m.x == -INFINITY ? 0.f : ex2(m.x - top);
+      sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+      l = fmaf(f, m.y, l);
     }
+  }
+  sums[rt][share][q4] = sum;
+  if (q4 == 0) ls[rt][share] = l;
+  __syncthreads();
+  if (share == 0 && live) {
     l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kShares; k++) l += ls[k];
+    for (int k = 0; k < kShares; k++) l += ls[rt][k];
+#pragma unroll
+    for (int k = 1; k < kShares; k++) {
+      const float4 v = sums[rt][k][q4];
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int qi = (d.row0 + r) / a.group, h = d.head0 + (d.row0 + r) % a.group;
     T* out = static_cast<T*>(a.out) + ((size_t)(d.q_row + qi) * a.h_q + h) * D + 4 * q4;
@@ -594,9 +602,12 @@ sf_status launch_decode(const KvpAttendArgs& a, cudaStream_t s) {
   da.a = a;
   da.desc = static_cast<KvpShared*>(a.ws);
   da.parts = reinterpret_cast<float*>(da.desc + ctas);
-  SF_CUDA(cudaFuncSetAttribute(kvp_decode_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  SF_CUDA((kvp_allow_smem<kvp_decode_kernel<T, D, NT>>(C::kSmem)));
   SF_CUDA(launch_pdl(kvp_decode_kernel<T, D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, s, da));
-  SF_CUDA(launch_pdl(kvp_merge_kernel<T, D, NT>, dim3(ctas, C::kRows), dim3(kThreads), 0, s, da));
+    // without cu_q the rows of every sequence are known
+  const int most = a.cu_q ? C::kRows : (int)std::min<long>((long)(a.n_q / a.batch) * a.group, C::kRows);
+  SF_CUDA(launch_pdl(kvp_merge_kernel<T, D, NT>, dim3(ctas, (most + kMergeRows - 1) / kMergeRows), dim3(kMergeThreads),
+                     0, s, da));
   return SF_OK;
 }
 

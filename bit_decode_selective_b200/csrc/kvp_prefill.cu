@@ -613,7 +613,7 @@ sf_status launch_prefill(const KvpAttendArgs& a, cudaStream_t s) {
   pa.a = a;
   pa.desc = static_cast<KvpShared*>(a.ws);
   pa.parts = reinterpret_cast<float*>(pa.desc + ctas);
-  SF_CUDA(cudaFuncSetAttribute(kvp_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  SF_CUDA((kvp_allow_smem<kvp_prefill_kernel<T, D>>(C::kSmem)));
   SF_CUDA(launch_pdl(kvp_prefill_kernel<T, D>, dim3(ctas), dim3(kThreads), C::kSmem, s, pa));
   SF_CUDA(launch_pdl(kvp_prefill_merge_kernel<T, D>, dim3(ctas, kRows / (kMergeThreads / (D / 4))), dim3(kMergeThreads),
                      0, s, pa));

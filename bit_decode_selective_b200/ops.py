@@ -234,10 +234,14 @@ class KVCache:
 
 _DTYPES = {torch.float16: abi.SF_F16, torch.bfloat16: abi.SF_BF16, torch.float32: abi.SF_F32}
 
+# The handle of a device's current stream, without a Stream object around it
+# (2 us less per call; single-token calls take a few).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-def _need(ok: bool, where: str, message: str) -> None:
-    if not ok:
-        raise abi.SFError(abi.SF_ERR_INVALID_ARG, where, message)
+
+def _refuse(where: str, message: str):
+    return abi.SFError(abi.SF_ERR_INVALID_ARG, where, message)
 
 
 class PagedKVCache:
@@ -252,31 +256,45 @@ class PagedKVCache:
         check(abi.sf_kvp_bytes(n_pages, page, h_kv, d, ctypes.byref(size)), "sf_kvp_bytes")
         if pool is None:
             pool = torch.zeros(size.value, dtype=torch.uint8, device=device)
-        _need(pool.is_cuda and pool.dtype == torch.uint8 and pool.is_contiguous() and pool.numel() == size.value,
-              "PagedKVCache", f"pool must be {size.value} contiguous uint8 on a CUDA device")
+        if not (pool.is_cuda and pool.dtype == torch.uint8 and pool.is_contiguous() and pool.numel() == size.value):
+            raise _refuse("PagedKVCache", f"pool must be {size.value} contiguous uint8 on a CUDA device")
         self.n_pages, self.page, self.h_kv, self.d, self.pool = n_pages, page, h_kv, d, pool
         self.device = pool.device
         self.desc = abi.sf_kvp(n_pages, page, h_kv, d, pool.data_ptr())
         self._ref = ctypes.byref(self.desc)
         self._ws_bytes = {}
 
-    def _index(self, t, where, name, shape):
-        _need(t.dtype == torch.int32 and t.device == self.device and t.is_contiguous()
-              and tuple(t.shape) == shape, where, f"{name} must be contiguous int32 of shape {shape} on {self.device}")
+    def _run(self, where, stream, *args):
+        """The entry point on `stream` (default: the current one) of the cache's device."""
+        fn = getattr(abi.lib(), where)
+        index = self.device.index
+        s = _current_stream(index) if stream is None else stream.cuda_stream
+        if torch.cuda.current_device() == index:
+            status = fn(self._ref, *args, s)
+        else:
+            with torch.cuda.device(index):
+                status = fn(self._ref, *args, s)
+        if status:
+            check(status, where)
+
+    def _index(self, t, where, name, *shape):
+        if t.dtype != torch.int32 or t.device != self.device or t.shape != shape or not t.is_contiguous():
+            raise _refuse(where, f"{name} must be contiguous int32 of shape {shape} on {self.device}")
         return t.data_ptr()
 
     def _rows(self, t, where, name, heads):
         """Pointer, row and head strides of [n][heads][d] rows with unit stride inside a head."""
-        _need(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == self.d and t.device == self.device
-              and (t.stride(2) == 1 or t.numel() == 0), where,
-              f"{name} must be [n][{heads}][{self.d}] on {self.device}, elements of a head consecutive")
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if heads > 1 else 0
+        shape, stride = t.shape, t.stride()
+        if (len(shape) != 3 or shape[1] != heads or shape[2] != self.d or t.device != self.device
+                or (stride[2] != 1 and shape[0])):
+            raise _refuse(where, f"{name} must be [n][{heads}][{self.d}] on {self.device}, elements of a head consecutive")
+        return t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if heads > 1 else 0
 
     def _bad(self, bad, where):
         if bad is None:
             return None
-        _need(bad.dtype == torch.int32 and bad.device == self.device and bad.numel() == 1, where,
-              "bad must be one int32 on the cache's device")
+        if bad.dtype != torch.int32 or bad.device != self.device or bad.numel() != 1:
+            raise _refuse(where, "bad must be one int32 on the cache's device")
         return bad.data_ptr()
 
     def write(self, k, v, slots, bad=None, stream=None):
@@ -285,40 +303,44 @@ class PagedKVCache:
         (one int32) counts slots outside the pool."""
         where = "sf_kvp_write"
         some = k if k is not None else v
-        _need(some is not None and some.dtype in _DTYPES and (v is None or v.dtype == some.dtype), where,
-              "k and v must be of one type: fp16, bf16 or fp32")
+        if some is None or some.dtype not in _DTYPES or some.dim() != 3:
+            raise _refuse(where, "k or v must be given, [n][h_kv][d] of fp16, bf16 or fp32")
         n = some.shape[0]
-        _need(v is None or v.shape[0] == n, where, "k and v must hold the same number of tokens")
-        kp = self._rows(k, where, "k", self.h_kv) if k is not None else (None, 0, 0)
-        vp = self._rows(v, where, "v", self.h_kv) if v is not None else (None, 0, 0)
-        with torch.cuda.device(self.device):
-            check(abi.sf_kvp_write(self._ref, *kp, *vp, _DTYPES[some.dtype], n,
-                                   self._index(slots, where, "slots", (n,)), self._bad(bad, where), _stream(stream)),
-                  where)
+        if v is not None and (v.dtype != some.dtype or v.shape[0] != n):
+            raise _refuse(where, "k and v must be of one type and number of tokens")
+        kp, kr, kh = self._rows(k, where, "k", self.h_kv) if k is not None else (None, 0, 0)
+        vp, vr, vh = self._rows(v, where, "v", self.h_kv) if v is not None else (None, 0, 0)
+        self._run(where, stream, kp, kr, kh, vp, vr, vh, _DTYPES[some.dtype], n,
+                  self._index(slots, where, "slots", n), self._bad(bad, where))
 
     def read(self, slots, dtype=torch.float16, k=None, v=None, bad=None, stream=None):
         """The values of `slots` [n] int32: (k, v), each [n][h_kv][d] of `dtype`
         (sf_kvp_read).  Rows of -1 and of slots outside the pool are zeros."""
         where = "sf_kvp_read"
-        _need(dtype in _DTYPES, where, "dtype must be fp16, bf16 or fp32")
+        if dtype not in _DTYPES:
+            raise _refuse(where, "dtype must be fp16, bf16 or fp32")
         n = slots.numel()
         shape = (n, self.h_kv, self.d)
-        out = []
-        for t, name in ((k, "k"), (v, "v")):
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=self.device)
-            _need(t.dtype == dtype and tuple(t.shape) == shape and t.is_contiguous() and t.device == self.device,
-                  where, f"{name} must be contiguous {dtype} of shape {shape} on {self.device}")
-            out.append(t)
-        with torch.cuda.device(self.device):
-            check(abi.sf_kvp_read(self._ref, self._index(slots, where, "slots", (n,)), n, out[0].data_ptr(),
-                                  out[1].data_ptr(), _DTYPES[dtype], self._bad(bad, where), _stream(stream)), where)
-        return out[0], out[1]
+        k, v = (self._out(t, where, name, shape, dtype, stream) for t, name in ((k, "k"), (v, "v")))
+        self._run(where, stream, self._index(slots, where, "slots", n), n, k.data_ptr(), v.data_ptr(), _DTYPES[dtype],
+                  self._bad(bad, where))
+        return k, v
+
+    def _out(self, t, where, name, shape, dtype, stream):
+        """An output of the given shape: `t` where it is given, else a new tensor."""
+        if t is None:
+            t = self.pool.new_empty(shape, dtype=dtype)
+            if stream is not None:
+                t.record_stream(stream)
+        elif t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            raise _refuse(where, f"{name} must be contiguous {dtype} of shape {tuple(shape)} on {self.device}")
+        return t
 
     def attend_workspace(self, n_q: int, batch: int, h_q: int) -> int:
         key = (n_q, batch, h_q)
         if key not in self._ws_bytes:
-            self._ws_bytes[key] = abi.sf_kvp_attend_workspace_bytes(self._ref, n_q, batch, h_q)
+            with torch.cuda.device(self.device):
+                self._ws_bytes[key] = abi.sf_kvp_attend_workspace_bytes(self._ref, n_q, batch, h_q)
         return self._ws_bytes[key]
 
     def attend(self, q, pages, lens, cu_q=None, scale=None, window: int = 0, sinks: int = 0, out=None, bad=None,
@@ -330,25 +352,21 @@ class PagedKVCache:
         the tokens up to its own, with window > 0 only the last `window` of them
         and the first `sinks`.  Returns out [n_q][h_q][d]."""
         where = "sf_kvp_attend"
-        _need(q.dim() == 3 and q.dtype in _DTYPES, where, "q must be [n_q][h_q][d], fp16 or bf16")
-        n_q, h_q = q.shape[0], q.shape[1]
-        qp = self._rows(q, where, "q", h_q)
-        _need(lens.dim() == 1 and pages.dim() == 2, where, "lens must be [batch], pages [batch][max_pages]")
-        batch, max_pages = lens.shape[0], pages.shape[1]
-        if out is None:
-            out = torch.empty((n_q, h_q, self.d), dtype=q.dtype, device=self.device)
-        _need(out.dtype == q.dtype and tuple(out.shape) == (n_q, h_q, self.d) and out.is_contiguous()
-              and out.device == self.device, where, "out must be contiguous, of q's type and shape")
-        with torch.cuda.device(self.device):
-            if ws is None:
-                ws = torch.empty(max(self.attend_workspace(n_q, batch, h_q), 16), dtype=torch.uint8,
-                                 device=self.device)
-                if stream is not None:
-                    ws.record_stream(stream)
-            check(abi.sf_kvp_attend(self._ref, *qp, _DTYPES[q.dtype], n_q,
-                                    None if cu_q is None else self._index(cu_q, where, "cu_q", (batch + 1,)),
-                                    self._index(pages, where, "pages", (batch, max_pages)), max_pages,
-                                    self._index(lens, where, "lens", (batch,)), batch, h_q,
-                                    self.d ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-                                    self._bad(bad, where), ws.data_ptr(), ws.numel(), _stream(stream)), where)
+        if q.dim() != 3 or q.dtype not in _DTYPES:
+            raise _refuse(where, "q must be [n_q][h_q][d], fp16 or bf16")
+        if lens.dim() != 1 or pages.dim() != 2:
+            raise _refuse(where, "lens must be [batch], pages [batch][max_pages]")
+        n_q, h_q, _ = q.shape
+        batch, max_pages = pages.shape
+        qp, qr, qh = self._rows(q, where, "q", h_q)
+        out = self._out(out, where, "out", q.shape, q.dtype, stream)
+        if ws is None:
+            ws = self._out(None, where, "ws", (max(self.attend_workspace(n_q, batch, h_q), 16),), torch.uint8, stream)
+        elif ws.device != self.device or not ws.is_contiguous():
+            raise _refuse(where, "ws must be contiguous, on the cache's device")
+        self._run(where, stream, qp, qr, qh, _DTYPES[q.dtype], n_q,
+                  None if cu_q is None else self._index(cu_q, where, "cu_q", batch + 1),
+                  self._index(pages, where, "pages", batch, max_pages), max_pages,
+                  self._index(lens, where, "lens", batch), batch, h_q, self.d ** -0.5 if scale is None else scale,
+                  window, sinks, out.data_ptr(), self._bad(bad, where), ws.data_ptr(), ws.nbytes)
         return out
