@@ -6,9 +6,11 @@
 // (include/sf.h).  The decisions are those of fp64 arithmetic with one rounding
 // per operation (quant.cuh).
 //
-// Four neighbouring lanes hold a group, 8 elements each (one 16-byte load of a
-// 16-bit type, two of fp32): min and max take two shuffles, and a lane's 8
-// codes are one 32-bit word of the tile.
+// A thread takes one token of one head, and of every group the quarter that its
+// place c among four neighbouring lanes names: 8 elements, one 16-byte load or
+// store of a 16-bit type, one 32-bit word of codes.  The eight tokens of a warp
+// then touch whole sectors on both sides: 64 bytes of a row, and 128 bytes of a
+// tile's codes where their slots follow each other.
 #include <climits>
 
 #include "kvp.cuh"
@@ -22,6 +24,7 @@ sf_status check_kvp(const sf_kvp* kv) {
   SF_UNSUPPORTED(kv->d == 64 || kv->d == 128, "a paged cache has d 64 or 128 (got %d)", kv->d);
   SF_UNSUPPORTED(kv->page >= 16 && kv->page <= 1024 && (kv->page & (kv->page - 1)) == 0,
                  "page=%d is not a power of two in [16, 1024]", kv->page);
+  SF_UNSUPPORTED(kv->h_kv <= 65535, "h_kv=%d above 65535", kv->h_kv);
   SF_UNSUPPORTED((long long)kv->n_pages * kv->page <= INT_MAX, "%d pages of %d tokens pass 2^31 slots", kv->n_pages,
                  kv->page);
   SF_REQUIRE(kv->pool && aligned16(kv->pool), "pool must be a non-null 16-byte aligned device pointer");
@@ -31,6 +34,7 @@ sf_status check_kvp(const sf_kvp* kv) {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTokens = kThreads / 4;  // per CTA
 
 struct CacheArgs {
   uint8_t* pool;
@@ -40,7 +44,7 @@ struct CacheArgs {
   const int32_t* slots;
   int32_t* bad;
   int n, h_kv, page_shift, n_slots;
-  int kind0;  // blockIdx.y = 0 handles kind kind0 (0 keys, 1 values)
+  int kind0;  // kind of blockIdx.z = 0 (0 keys, 1 values)
 };
 
 // Byte offset of the tile that holds `slot` for head h.
@@ -50,9 +54,52 @@ __device__ __forceinline__ size_t tile_offset(int slot, int h, int h_kv, int pag
   return (((size_t)page * h_kv + h << (page_shift - 4)) + (in_page >> 4)) * KvpTile<D>::kBytes;
 }
 
+// NaN to 0, everything else into +-kKvpLimit.
 __device__ __forceinline__ float tame(float x) {
-  x = fminf(fmaxf(x, -kKvpLimit), kKvpLimit);
-  return x;
+  return isnan(x) ? 0.f : fminf(fmaxf(x, -kKvpLimit), kKvpLimit);
+}
+
+// The step of a group whose values span lo .. hi, fp16((hi - lo) / 15) in one
+// rounding from fp64.  In fp32 the quotient is within 2^-22 of itself of the
+// fp64 one; where that could round to another fp16 it is taken in fp64.
+__device__ __forceinline__ uint16_t step16(float lo, float hi) {
+  const float x = (hi - lo) * (1.f / 15.f);
+  const uint16_t a = __half_as_ushort(__float2half_rn(x * (1.f - 0x1p-21f)));
+  const uint16_t b = __half_as_ushort(__float2half_rn(x * (1.f + 0x1p-21f)));
+  return a == b ? a : group_grid((double)lo, (double)hi, 4).s16;
+}
+
+// The codes of 8 values as a word, floor((v - m) / s + 1/2) clamped to 0 .. 15
+// as fp64 arithmetic decides.  fp32 finds (v - m) / s < 24 to 2^-22 of itself,
+// 6e-6: only values closer than 2e-5 to a border are decided in fp64.
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint16_t s16, uint16_t m16) {
+  if (s16 == 0) return 0u;
+  const float m = h2f(m16), inv = __frcp_rn(h2f(s16));
+  uint32_t word = 0;
+  bool near_border = false;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float u = fmaf(v[i] - m, inv, 0.5f);
+    // rounding down at 2^23 leaves floor(u) in the mantissa
+    const float c = fminf(fmaxf(u, 0.f), 15.5f);
+    const float r = __fadd_rd(c, 8388608.f);
+    const float frac = u - (r - 8388608.f);  // outside [0, 1) only where c was clamped
+    near_border = near_border || fabsf(frac) < 2e-5f || fabsf(frac - 1.f) < 2e-5f;
+    word |= (__float_as_uint(r) & 15u) << (4 * i);
+  }
+  if (near_border) {
+    Grid16 g;
+    g.s16 = s16, g.m16 = m16, g.S = h2d(s16), g.M = h2d(m16);
+    word = 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; i++) {
+      float x = v[0];
+#pragma unroll
+      for (int k = 1; k < 8; k++) x = i == k ? v[k] : x;
+      word |= (uint32_t)nested_code((double)x, g, 0, 15) << (4 * i);
+    }
+  }
+  return word;
 }
 
 template <typename T>
@@ -86,99 +133,119 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
   }
 }
 
-// One thread: 8 elements of one (token, head); D / 8 threads a row.
+// blockIdx: (64 tokens, head, keys or values).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kvp_write_kernel(CacheArgs a) {
+__global__ void __launch_bounds__(kThreads) kvp_write_kernel(const __grid_constant__ CacheArgs a) {
   using L = KvpTile<D>;
+  constexpr int G = L::G;
   pdl_trigger();
   pdl_wait();
-  const int kind = a.kind0 + blockIdx.y;
-  const long unit = (long)blockIdx.x * kThreads + threadIdx.x;
-  const long row = unit / (D / 8);
-  const int part = (int)(unit % (D / 8));  // 8-element part of the row
-  const long tok = row / a.h_kv;
-  const int h = (int)(row % a.h_kv);
-  const bool in = tok < a.n;
-  const int slot = in ? a.slots[tok] : -1;
+  const int kind = a.kind0 + blockIdx.z, h = blockIdx.y, c = threadIdx.x & 3;
+  const int tok = blockIdx.x * kTokens + (threadIdx.x >> 2);
+  const int slot = tok < a.n ? a.slots[tok] : -1;
   const bool ok = slot >= 0 && slot < a.n_slots;
-  if (in && !ok && slot != -1 && a.bad && blockIdx.y == 0 && h == 0 && part == 0) atomicAdd(a.bad, 1);
-  float v[8];
+  if (!ok && slot != -1 && a.bad && c == 0 && h == 0 && blockIdx.z == 0) atomicAdd(a.bad, 1);
+  float v[G][8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = 0.f;
-  if (ok) load8<T>(a.x[kind], tok * a.row[kind] + h * a.head[kind] + part * 8, v);
-  float lo = INFINITY, hi = -INFINITY;
+  for (int g = 0; g < G; g++)
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    v[i] = isnan(v[i]) ? 0.f : tame(v[i]);
-    lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]);
+    for (int i = 0; i < 8; i++) v[g][i] = 0.f;
+  if (ok) {
+#pragma unroll
+    for (int g = 0; g < G; g++) load8<T>(a.x[kind], tok * a.row[kind] + h * a.head[kind] + g * 32 + c * 8, v[g]);
   }
+  uint8_t* tile = a.pool + (ok ? tile_offset<D>(slot, h, a.h_kv, a.page_shift) : 0);
+  const int t = slot & 15;
+  uint32_t grid = 0;  // (s, m) of group c, or of group c % 2 where there are two
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  if (!ok) return;
-  const Grid16 g = group_grid((double)lo, (double)hi, 4);
-  uint32_t word = 0;
+  for (int g = 0; g < G; g++) {
+    float lo = v[g][0], hi = v[g][0], odd = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) word |= (uint32_t)nested_code((double)v[i], g, 0, 15) << (4 * i);
-  uint8_t* tile = a.pool + tile_offset<D>(slot, h, a.h_kv, a.page_shift);
-  const int grp = part >> 2, t = slot & 15;
-  *reinterpret_cast<uint32_t*>(tile + (kind ? L::kValueCodes : L::kKeyCodes) + (grp * 16 + t) * 16 + (part & 3) * 4) =
-      word;
-  if ((part & 3) == 0) {
-    if (kind) {
-      uint16_t* vz = reinterpret_cast<uint16_t*>(tile + L::kValueGrid) + ((t >> 1) * L::G + grp) * 4 + (t & 1);
-      vz[0] = g.s16, vz[2] = g.m16;
-    } else {
-      *reinterpret_cast<uint32_t*>(tile + L::kKeyGrid + (t * L::G + grp) * 4) =
-          (uint32_t)g.s16 | ((uint32_t)g.m16 << 16);
+    for (int i = 0; i < 8; i++) {
+      lo = fminf(lo, v[g][i]), hi = fmaxf(hi, v[g][i]);
+      odd = fmaf(v[g][i], 0.f, odd);  // NaN if some value is not finite
     }
+    if (!(odd == 0.f) || lo < -kKvpLimit || hi > kKvpLimit) {
+      lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        v[g][i] = tame(v[g][i]);
+        lo = fminf(lo, v[g][i]), hi = fmaxf(hi, v[g][i]);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    const uint16_t s16 = step16(lo, hi), m16 = __half_as_ushort(__float2half_rn(lo));
+    const uint32_t word = codes8(v[g], s16, m16);
+    if (ok)
+      *reinterpret_cast<uint32_t*>(tile + (kind ? L::kValueCodes : L::kKeyCodes) + (g * 16 + t) * 16 + c * 4) = word;
+    if (c == g) grid = (uint32_t)s16 | ((uint32_t)m16 << 16);
+  }
+  if (!ok || c >= G) return;
+  if (kind) {
+    uint16_t* vz = reinterpret_cast<uint16_t*>(tile + L::kValueGrid) + ((t >> 1) * G + c) * 4 + (t & 1);
+    vz[0] = (uint16_t)(grid & 0xffff), vz[2] = (uint16_t)(grid >> 16);
+  } else {
+    *reinterpret_cast<uint32_t*>(tile + L::kKeyGrid + (t * G + c) * 4) = grid;
   }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kvp_read_kernel(CacheArgs a) {
+__global__ void __launch_bounds__(kThreads) kvp_read_kernel(const __grid_constant__ CacheArgs a) {
   using L = KvpTile<D>;
+  constexpr int G = L::G;
   pdl_trigger();
   pdl_wait();
-  const int kind = a.kind0 + blockIdx.y;
-  const long unit = (long)blockIdx.x * kThreads + threadIdx.x;
-  const long row = unit / (D / 8);
-  const int part = (int)(unit % (D / 8));
-  const long tok = row / a.h_kv;
-  const int h = (int)(row % a.h_kv);
+  const int kind = a.kind0 + blockIdx.z, h = blockIdx.y, c = threadIdx.x & 3;
+  const int tok = blockIdx.x * kTokens + (threadIdx.x >> 2);
   if (tok >= a.n) return;
   const int slot = a.slots[tok];
   const bool ok = slot >= 0 && slot < a.n_slots;
-  if (!ok && slot != -1 && a.bad && blockIdx.y == 0 && h == 0 && part == 0) atomicAdd(a.bad, 1);
-  float v[8];
+  if (!ok && slot != -1 && a.bad && c == 0 && h == 0 && blockIdx.z == 0) atomicAdd(a.bad, 1);
+  uint32_t word[G], s[G], m[G];  // fp16 bits
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = 0.f;
+  for (int g = 0; g < G; g++) word[g] = s[g] = m[g] = 0u;
   if (ok) {
     const uint8_t* tile = a.pool + tile_offset<D>(slot, h, a.h_kv, a.page_shift);
-    const int grp = part >> 2, t = slot & 15;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(tile + (kind ? L::kValueCodes : L::kKeyCodes) +
-                                                             (grp * 16 + t) * 16 + (part & 3) * 4);
-    float s, m;
-    if (kind) {
-      const uint16_t* vz =
-          reinterpret_cast<const uint16_t*>(tile + L::kValueGrid) + ((t >> 1) * L::G + grp) * 4 + (t & 1);
-      s = h2f(vz[0]), m = h2f(vz[2]);
-    } else {
-      const uint32_t z = *reinterpret_cast<const uint32_t*>(tile + L::kKeyGrid + (t * L::G + grp) * 4);
-      s = h2f((uint16_t)(z & 0xffff)), m = h2f((uint16_t)(z >> 16));
-    }
+    const int t = slot & 15;
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] = fmaf((float)((word >> (4 * i)) & 15u), s, m);
+    for (int g = 0; g < G; g++)
+      word[g] = *reinterpret_cast<const uint32_t*>(tile + (kind ? L::kValueCodes : L::kKeyCodes) + (g * 16 + t) * 16 +
+                                                   c * 4);
+    if (kind) {
+      const uint4* p = reinterpret_cast<const uint4*>(tile + L::kValueGrid + (t >> 1) * (8 * G));
+      const int sh = (t & 1) * 16;
+#pragma unroll
+      for (int g = 0; g < G; g += 2) {
+        const uint4 z = p[g / 2];
+        s[g] = z.x >> sh, m[g] = z.y >> sh, s[g + 1] = z.z >> sh, m[g + 1] = z.w >> sh;
+      }
+    } else {
+      const uint2* p = reinterpret_cast<const uint2*>(tile + L::kKeyGrid + t * (4 * G));
+#pragma unroll
+      for (int g = 0; g < G; g += 2) {
+        const uint2 z = p[g / 2];
+        s[g] = z.x, m[g] = z.x >> 16, s[g + 1] = z.y, m[g + 1] = z.y >> 16;
+      }
+    }
   }
-  store8<T>(a.y[kind], row * D + part * 8, v);
+  const int64_t at = ((int64_t)tok * a.h_kv + h) * D + c * 8;
+#pragma unroll
+  for (int g = 0; g < G; g++) {
+    const float sf = h2f((uint16_t)s[g]), mf = h2f((uint16_t)m[g]);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = fmaf((float)((word[g] >> (4 * i)) & 15u), sf, mf);
+    store8<T>(a.y[kind], at + g * 32, v);
+  }
 }
 
 template <typename T>
 sf_status launch_cache(const CacheArgs& a, int d, int kinds, bool read, cudaStream_t s) {
-  const long units = (long)a.n * a.h_kv * (d / 8);
-  const dim3 grid((unsigned)((units + kThreads - 1) / kThreads), kinds);
+  const dim3 grid((a.n + kTokens - 1) / kTokens, a.h_kv, kinds);
   if (d == 128)
     SF_CUDA(launch_pdl(read ? kvp_read_kernel<T, 128> : kvp_write_kernel<T, 128>, grid, dim3(kThreads), 0, s, a));
   else
@@ -215,7 +282,6 @@ sf_status check_slots(const sf_kvp* kv, const int32_t* slots, int n, sf_dtype dt
   SF_REQUIRE(n >= 0, "n=%d < 0", n);
   SF_REQUIRE(n == 0 || (slots && ((uintptr_t)slots & 3) == 0), "slots must be a non-null 4-byte aligned device pointer");
   SF_REQUIRE(((uintptr_t)bad & 3) == 0, "bad must be 4-byte aligned");
-  SF_UNSUPPORTED((long long)n * kv->h_kv * (kv->d / 8) <= (long long)INT_MAX * kThreads, "n=%d is too large", n);
   return SF_OK;
 }
 
