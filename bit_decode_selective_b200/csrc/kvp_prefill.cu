@@ -144,22 +144,48 @@ __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
-      "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(addr)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// Two fp32 values in a register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 split(uint64_t p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -266,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
       const int row0 = it.rt * kRows, rows = min(it.seq.n * a.group - row0, kRows);
       if (t == 0 || rows > kTileRows) {
         const int rr = row0 + min(r, rows - 1);
-        const int qi = it.seq.q0 + rr / a.group, head = it.g * a.group + rr % a.group;
         const int pos = it.seq.len - it.seq.n + rr / a.group;
         // ---- the row's query, scaled into fp16's range
-        const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + qi * a.q_row + head * a.q_head);
+        const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (it.seq.q0 + rr / a.group) * a.q_row +
+                                                         (it.g * a.group + rr % a.group) * a.q_head);
         float top = 0.f;
 #pragma unroll 4
         for (int i = 0; i < D / 8; i++) {
@@ -282,8 +308,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
           }
         }
         const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 100);
-        const float up = r < rows ? __uint_as_float((uint32_t)(127 + 10 - e) << 23) : 0.f;
-        const float kappa = __uint_as_float((uint32_t)(127 - 10 + e) << 23) * a.scale_log2;
+        // a negative scale turns the query around and a scale of 0 becomes one
+        // that rounds away, so that the largest S is the largest logit
+        const float up = r < rows ? copysignf(__uint_as_float((uint32_t)(127 + 10 - e) << 23), a.scale_log2) : 0.f;
+        const float kappa = fmaxf(__uint_as_float((uint32_t)(127 - 10 + e) << 23) * fabsf(a.scale_log2), 1e-37f);
 #pragma unroll 4
         for (int i = 0; i < D / 8; i++) {
           const uint4 w = qr[i];
@@ -309,56 +337,59 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
           const int4 pl1 = *reinterpret_cast<const int4*>(&ctl.place[ring][4]);
           const int place[kStep] = {pl0.x, pl0.y, pl0.z, pl0.w, pl1.x, pl1.y, pl1.z, pl1.w};
           const bool whole = (place[0] & place[1] & place[2] & place[3] & place[4] & place[5] & place[6] & place[7]) & 1;
-          uint32_t p[kTokens / 2];
-          float sum;
-          for (;;) {
-            // weights against the present reference; done again when a logit passes it too far
-            const float off = (ref == -INFINITY ? 0.f : ref) - kRefShift;
-            float ymax = -INFINITY;
-            sum = 0.f;
+          uint32_t s[kTokens / 32][32];
+#pragma unroll
+          for (int ch = 0; ch < kTokens / 32; ch++) tc_ld32(s[ch], s_at + ch * 32);
+          tc_wait_ld();
+          if (!whole) {
 #pragma unroll
             for (int ch = 0; ch < kTokens / 32; ch++) {
-              uint32_t s[32];
-              tc_ld32(s, s_at + ch * 32);
-              tc_wait_ld();
-              float y[32];
+              const uint32_t seen = seen16(a, pos, place[2 * ch] & ~1) | (seen16(a, pos, place[2 * ch + 1] & ~1) << 16);
 #pragma unroll
-              for (int i = 0; i < 32; i++) y[i] = fmaf(__uint_as_float(s[i]), kappa, -off);
-              if (!whole) {
-                const uint32_t seen = seen16(a, pos, place[2 * ch] & ~1) | (seen16(a, pos, place[2 * ch + 1] & ~1) << 16);
-#pragma unroll
-                for (int i = 0; i < 32; i++) y[i] = seen >> i & 1 ? y[i] : -INFINITY;
-              }
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                ymax = fmaxf(ymax, fmaxf(y[i], y[i + 1]));
-                const float p0 = ex2(y[i]), p1 = ex2(y[i + 1]);
-                sum += p0 + p1;
-                p[ch * 16 + i / 2] = pack2(p0, p1);
-              }
+              for (int i = 0; i < 32; i++) s[ch][i] = seen >> i & 1 ? s[ch][i] : 0xff800000u;  // -infinity
             }
-            const float top2 = ymax + off;
-            if (!__any_sync(0xffffffffu, top2 > ref + kRefGap)) break;
-            const float next = fmaxf(ref, top2);
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int ch = 0; ch < kTokens / 32; ch++)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              top = fmaxf(top, fmaxf(__uint_as_float(s[ch][i]), __uint_as_float(s[ch][i + 1])));
+          top *= kappa;
+          if (__any_sync(0xffffffffu, top > ref + kRefGap)) {
+            const float next = fmaxf(ref, top);
             const float f = next == -INFINITY ? 1.f : ex2(ref - next);
             ref = next;
             l *= f;
             if (j > s0) {  // the products into O so far are complete: S was issued after them
 #pragma unroll
-              for (int ch = 0; ch < D / 32; ch++) {
-                uint32_t o[32];
-                tc_ld32(o, o_at + ch * 32);
+              for (int ch = 0; ch < D / 16; ch++) {
+                uint32_t o[16];
+                tc_ld16(o, o_at + ch * 16);
                 tc_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tc_st32(o_at + ch * 32, o);
+                for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tc_st16(o_at + ch * 16, o);
               }
-              tc_wait_st();
             }
           }
-          l += sum;
-          tc_st32(s_at, p);
-          tc_st32(s_at + 32, p + 32);
+          const float off = kRefShift - (ref == -INFINITY ? 0.f : ref);
+          uint64_t sums = 0;  // two fp32 sums
+          const uint64_t kk = pair(kappa, kappa), oo = pair(off, off);
+#pragma unroll
+          for (int ch = 0; ch < kTokens / 32; ch++) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = split(fma2(pair(__uint_as_float(s[ch][i]), __uint_as_float(s[ch][i + 1])), kk, oo));
+              const float p0 = ex2(y.x), p1 = ex2(y.y);
+              sums = add2(sums, pair(p0, p1));
+              p[i / 2] = pack2(p0, p1);
+            }
+            tc_st16(s_at + ch * 16, p);
+          }
+          const float2 sum = split(sums);
+          l += sum.x + sum.y;
           tc_wait_st();
           tc_before();
           mbar_arrive(&ctl.p_full[t]);
@@ -371,7 +402,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         const bool all = s0 == 0 && s1 == it.steps;
         float* part = pa.parts + (size_t)(2 * blockIdx.x + (range.u0 > at ? 0 : 1)) * C::kPartFloats;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
-        T* out = static_cast<T*>(a.out) + ((size_t)qi * a.h_q + head) * D;
+        T* out = static_cast<T*>(a.out) +
+                 ((size_t)(it.seq.q0 + rr / a.group) * a.h_q + it.g * a.group + rr % a.group) * D;
 #pragma unroll
         for (int ch = 0; ch < D / 32; ch++) {
           uint32_t o[32];
