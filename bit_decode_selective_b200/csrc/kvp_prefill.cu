@@ -119,19 +119,29 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// One product step (K = 16).  The descriptors' upper halves are constants, the
+// lower ones differ by constants: the whole warp computes them, so that they
+// stay in uniform registers, and one elected lane issues.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi,
+                                          uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %6, 0;\n mov.b64 da, {%1, %3};\n mov.b64 db, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(add)
       : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                          uint32_t add) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %5, 0;\n mov.b64 db, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add)
       : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t is;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(is));
+  return is != 0;
 }
 __device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
   asm volatile(
@@ -194,14 +204,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
 
-// Descriptor of a 128-byte swizzled operand.  Contraction along the rows'
-// bytes (queries, keys): `far` unused, 8-row groups 1024 bytes apart.
-// Contraction along the rows (values): 64-element halves `far` bytes apart,
-// 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t far) {
-  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(far >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
+// Descriptor of a 128-byte swizzled operand, 8-row groups 1024 bytes apart:
+// lower half (address, `far`) and upper half.  Contraction along the rows'
+// bytes (queries, keys): `far` is not used.  Contraction along the rows
+// (values): 64-element halves lie `far` bytes apart.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t far) {
+  return ((addr >> 4) & 0x3FFF) | ((far >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t mma_desc(int n, bool b_by_rows) {  // fp16 x fp16 -> fp32, M = 128
   return (1u << 4) | (b_by_rows ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
@@ -543,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
   } else {
     regs_down<kIssueRegs>();
     // ======================= the products =====================================
-    if (warp == kSoftWarps + kFillWarps && lane == 0) {
+    if (warp == kSoftWarps + kFillWarps) {
       constexpr uint32_t kS = mma_desc(kTokens, false), kO = mma_desc(D, true);
       int n_q[2] = {0, 0}, n_p[2] = {0, 0};  // phases of q_full, p_full
       for (;;) {
@@ -558,27 +568,35 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
               if (t == 0) mbar_wait(&ctl.v_full[bst], (b >> 1) & 1, &ctl.gave_up);
               mbar_wait(&ctl.p_full[t], n_p[t]++ & 1, &ctl.gave_up);
               tc_after();
-              const uint32_t v_at = smem_at + C::kV + bst * C::kTileBytes;
-  #pragma unroll
-              for (int ks = 0; ks < kTokens / 16; ks++)
-                tc_mma_ts(tmem + 256 + t * D, tmem + t * 128 + ks * 8, smem_desc(v_at + ks * 2048, 16384), kO,
-                          j - 1 > s0 || ks > 0);
-              if (t == tiles - 1) tc_commit(&ctl.v_empty[bst]);
-              if (j == s1) tc_commit(&ctl.o_done[t]);
+              const uint32_t v_lo = desc_lo(smem_at + C::kV + bst * C::kTileBytes, 16384);
+              const uint32_t o_at = tmem + 256 + t * D, p_at = tmem + t * 128;
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < kTokens / 16; ks++)
+                  tc_mma_ts(o_at, p_at + ks * 8, v_lo + ks * (2048 >> 4), kDescHi, kO, ks > 0 || j - 1 > s0);
+                if (t == tiles - 1) tc_commit(&ctl.v_empty[bst]);
+                if (j == s1) tc_commit(&ctl.o_done[t]);
+              }
+              __syncwarp();
             }
             if (j < s1) {  // S = Q K
               if (j == s0) {
                 mbar_wait(&ctl.q_full[t], n_q[t]++ & 1, &ctl.gave_up);
                 tc_after();
               }
-              const uint32_t q_at = smem_at + C::kQ + t * C::kTileBytes, k_at = smem_at + C::kK + st * C::kTileBytes;
-  #pragma unroll
-              for (int ks = 0; ks < D / 16; ks++) {
-                const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-                tc_mma_ss(tmem + t * 128, smem_desc(q_at + off, 16), smem_desc(k_at + off, 16), kS, ks > 0);
+              const uint32_t q_lo = desc_lo(smem_at + C::kQ + t * C::kTileBytes, 16);
+              const uint32_t k_lo = desc_lo(smem_at + C::kK + st * C::kTileBytes, 16);
+              const uint32_t s_at = tmem + t * 128;
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                  const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                  tc_mma_ss(s_at, q_lo + off, k_lo + off, kDescHi, kDescHi, kS, ks > 0);
+                }
+                tc_commit(&ctl.s_full[t]);
+                if (t == tiles - 1) tc_commit(&ctl.k_empty[st]);
               }
-              tc_commit(&ctl.s_full[t]);
-              if (t == tiles - 1) tc_commit(&ctl.k_empty[st]);
+              __syncwarp();
             }
           }
         }
@@ -587,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         at += it.steps;
         it.next(a);
       }
-      tc_commit(&ctl.last);  // nothing is in flight when TMEM is given back
+      if (elect_one()) tc_commit(&ctl.last);  // nothing is in flight when TMEM is given back
+      __syncwarp();
       for (unsigned long long t0 = now_ns(); !mbar_try(&ctl.last, 0) && now_ns() - t0 < kWaitNs;) {
       }
     }
