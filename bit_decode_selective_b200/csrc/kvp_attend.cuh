@@ -89,13 +89,15 @@ __device__ __forceinline__ KvpSpan kvp_span(const KvpAttendArgs& a, int p0, int 
 // ---- the cut of the work ----------------------------------------------------
 //
 // An item is (sequence, tile of ROWS query rows, KV head); its work is counted
-// in steps of STEP cache tiles.  The items lie end to end (sequences, row tiles,
+// in steps of STEP cache tiles, after EXTRA steps' worth of time for its queries
+// and outputs.  The items lie end to end (sequences, row tiles,
 // KV heads, in that order) and the line of steps is cut into equal ranges, one
 // per CTA, on the device: the host needs no length.  Parts of an item that
 // several CTAs share are joined by a merge kernel in the order of the CTAs.
 // FEW: the sequences of at most few_rows rows, else the others.
-template <int ROWS, int STEP, bool FEW>
+template <int ROWS, int STEP, int EXTRA, bool FEW>
 struct KvpItem {
+  static constexpr int kExtra = EXTRA;
   int b, rt, g;
   KvpSeq seq;
   KvpSpan span;
@@ -114,8 +116,15 @@ struct KvpItem {
   static __device__ __forceinline__ long seq_steps(const KvpAttendArgs& a, const KvpSeq& s) {
     const int n = row_tiles(a, s);
     long sum = 0;
-    for (int rt = 0; rt < n; rt++) sum += steps_of(span_of(a, s, rt));
+    for (int rt = 0; rt < n; rt++) sum += EXTRA + steps_of(span_of(a, s, rt));
     return sum;
+  }
+  // The end of the item that starts at `at`, and the steps of it [s0, s1) that
+  // lie in [u0, u1) (none: s0 == s1).
+  __device__ __forceinline__ long end(long at) const { return at + EXTRA + steps; }
+  __device__ __forceinline__ int2 part(long at, long u0, long u1) const {
+    const int s0 = (int)min(max(u0 - at - EXTRA, 0l), (long)steps), s1 = (int)min(max(u1 - at - EXTRA, 0l), (long)steps);
+    return make_int2(s0, s1);
   }
   __device__ __forceinline__ void set(const KvpAttendArgs& a) {
     span = span_of(a, seq, rt);
@@ -143,10 +152,8 @@ struct KvpRangeShared {
   long at;
   int b, rt, g;
 };
-template <int THREADS, int ROWS, int STEP, bool FEW>
-__device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_steps, KvpRangeShared& sh,
-                                              KvpItem<ROWS, STEP, FEW>& it) {
-  using Item = KvpItem<ROWS, STEP, FEW>;
+template <int THREADS, typename Item>
+__device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_steps, KvpRangeShared& sh, Item& it) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long mine = 0;
   const int per = (a.batch + THREADS - 1) / THREADS;
@@ -178,7 +185,7 @@ __device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_st
       const KvpSeq s = kvp_seq(a, b);
       const int n = Item::row_tiles(a, s);
       for (int rt = 0; rt < n && !found; rt++) {
-        const int st = Item::steps_of(Item::span_of(a, s, rt));
+        const int st = Item::kExtra + Item::steps_of(Item::span_of(a, s, rt));
         if (r.u0 < at + (long)st * a.h_kv) {
           sh.b = b, sh.rt = rt, sh.g = (int)((r.u0 - at) / st);
           sh.at = at + (long)sh.g * st;
@@ -197,12 +204,13 @@ __device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_st
   return r;
 }
 
-// An item that several CTAs share, written by the one with its start.
+// An item that several CTAs share, written by the one with its first step.
 struct KvpShared {
   int q_row, row0, rows, head0;  // first query row of the sequence, first row, rows, first query head
   int parts, pad[3];
 };
-// How many CTAs share the item [at, at + steps) that starts in this one's range.
+// How many CTAs share the item that ends at `end` and has its first step in
+// this one's range.
 __device__ __forceinline__ int kvp_sharers(const KvpRange& r, long end) {
   long last = (end * r.ctas + r.total - 1) / r.total - 1;
   while (r.total * (last + 1) / r.ctas < end) last++;

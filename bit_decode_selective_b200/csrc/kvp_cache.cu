@@ -106,10 +106,10 @@ template <typename T>
 __device__ __forceinline__ void load8(const void* base, int64_t at, float (&v)[8]) {
   if constexpr (sizeof(T) == 4) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
+    const float4 a = __ldcg(p), b = __ldcg(p + 1);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at));
+    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(base) + at));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {

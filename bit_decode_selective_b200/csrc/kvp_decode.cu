@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepTiles = 2;  // tiles per warp and step
+constexpr int kExtra = 8;      // an item's queries, join and output take about as long as 8 steps of the CTA
 constexpr float kRefGap = 6.f;   // log2: how far a logit may pass the reference
 constexpr float kRefShift = 9.f; // weights are 2^(x - reference + 9) <= 2^15
 
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, c = lane & 3;
 
-  KvpItem<C::kRows, kStepTiles, true> it;
+  KvpItem<C::kRows, kStepTiles, kExtra, true> it;
   const KvpRange range = kvp_range<kThreads>(a, kWarps, range_sh, it);  // at least a step per warp
   if (tid == 0) da.desc[blockIdx.x].parts = 0;
   if (range.u0 == range.u1) return;
@@ -131,8 +132,10 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   const uint32_t stage0_u = smem_u32(stage0);
   uint2* qs = reinterpret_cast<uint2*>(smem + kWarps * C::kWarpBytes);  // NT > 1: the query operands
 
-  for (;;) {  // segments: this CTA's part of one item
-    const int s0 = (int)(max(u0, at) - at), s1 = (int)(min(u1, at + it.steps) - at);  // steps of the item
+  for (;; at = it.end(at), it.next(a)) {  // this CTA's part of each item
+    const int2 my = it.part(at, u0, u1);
+    const int s0 = my.x, s1 = my.y;
+    if (s0 == s1) break;  // the range ends before the item's first step
     const int rows_left = it.seq.n * a.group - it.rt * C::kRows, rows = min(rows_left, C::kRows);
     const int base = it.seq.len - it.seq.n, row0 = it.rt * C::kRows;
     const int32_t* pages = a.pages + (long)it.b * a.max_pages;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
       }
     __syncthreads();
     const bool all = s0 == 0 && s1 == it.steps;
-    float* part = da.parts + (size_t)(2 * blockIdx.x + (u0 > at ? 0 : 1)) * C::kPartFloats;
+    float* part = da.parts + (size_t)(2 * blockIdx.x + (s0 > 0 ? 0 : 1)) * C::kPartFloats;
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d4 = i % (D / 4) * 4;
       float top = -INFINITY;
@@ -515,14 +518,12 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
     if (!all && s0 == 0 && tid == 0) {
       KvpShared d;
       d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
-      d.parts = kvp_sharers(range, at + it.steps);
+      d.parts = kvp_sharers(range, it.end(at));
       d.pad[0] = d.pad[1] = d.pad[2] = 0;
       da.desc[blockIdx.x] = d;
     }
     __syncthreads();  // the exchange is read
-    if (at + it.steps >= u1) break;
-    at += it.steps;
-    it.next(a);
+    if (it.end(at) >= u1) break;
   }
 }
 

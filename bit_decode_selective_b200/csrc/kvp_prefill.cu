@@ -44,10 +44,11 @@ constexpr int kRing = 4;                 // steps whose token places are kept
 constexpr float kRefGap = 6.f, kRefShift = 9.f;
 constexpr unsigned long long kWaitNs = 1000000000ull;  // bounded waits give up after 1 s
 constexpr int kMinSteps = 1;
+constexpr int kExtra = 4;                // an item's queries and output take about as long as 4 steps
 
 __device__ unsigned int g_wait_timeouts;
 
-using Item = KvpItem<kRows, kStep, false>;
+using Item = KvpItem<kRows, kStep, kExtra, false>;
 
 template <int D>
 struct Cfg {
@@ -297,42 +298,51 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp & 3)
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
     int n_s = 0, n_o = 0;  // phases of s_full, o_done
-    for (;;) {
-      const int s0 = (int)(max(range.u0, at) - at), s1 = (int)(min(range.u1, at + it.steps) - at);
+    for (;; at = it.end(at), it.next(a)) {
+      const int2 my = it.part(at, range.u0, range.u1);
+      const int s0 = my.x, s1 = my.y;
+      if (s0 == s1) break;
       const int row0 = it.rt * kRows, rows = min(it.seq.n * a.group - row0, kRows);
       if (t == 0 || rows > kTileRows) {
         const int rr = row0 + min(r, rows - 1);
         const int pos = it.seq.len - it.seq.n + rr / a.group;
-        // ---- the row's query, scaled into fp16's range
-        const uint4* qr = reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (it.seq.q0 + rr / a.group) * a.q_row +
-                                                         (it.g * a.group + rr % a.group) * a.q_head);
-        float top = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; i++) {
-          const uint4 w = qr[i];
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        // ---- the tile's queries: D / 8 lanes a row, each row scaled by a power
+        // of two into fp16's range.  A negative scale turns the query around and
+        // a scale of 0 becomes one that rounds away, so that the largest S is
+        // the largest logit.
+        constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes;  // lanes a row, rows at a time
+        uint4 w[kLanes];
+        const int part8 = lane % kLanes, first_row = t * kTileRows + (warp & 3) * 32 + lane / kLanes;
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const float2 f = Elem<T>::to_float2(ws[e]);
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
+        for (int i = 0; i < kLanes; i++) {
+          const int x = row0 + min(first_row + i * kPerWarp, rows - 1);
+          w[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
+                                                      (it.seq.q0 + x / a.group) * a.q_row +
+                                                      (it.g * a.group + x % a.group) * a.q_head) + part8);
         }
-        const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 100);
-        // a negative scale turns the query around and a scale of 0 becomes one
-        // that rounds away, so that the largest S is the largest logit
-        const float up = r < rows ? copysignf(__uint_as_float((uint32_t)(127 + 10 - e) << 23), a.scale_log2) : 0.f;
-        const float kappa = fmaxf(__uint_as_float((uint32_t)(127 - 10 + e) << 23) * fabsf(a.scale_log2), 1e-37f);
-#pragma unroll 4
-        for (int i = 0; i < D / 8; i++) {
-          const uint4 w = qr[i];
-          const float2 f0 = Elem<T>::to_float2(w.x), f1 = Elem<T>::to_float2(w.y);
-          const float2 f2 = Elem<T>::to_float2(w.z), f3 = Elem<T>::to_float2(w.w);
+        int my_e = 0;
+#pragma unroll
+        for (int i = 0; i < kLanes; i++) {
+          const float2 f0 = Elem<T>::to_float2(w[i].x), f1 = Elem<T>::to_float2(w[i].y);
+          const float2 f2 = Elem<T>::to_float2(w[i].z), f3 = Elem<T>::to_float2(w[i].w);
+          float top = fmaxf(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))),
+                            fmaxf(fmaxf(fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y))));
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = min(max((int)((__float_as_uint(top) >> 23) & 255) - 127, -100), 100);
+          const int qrow = first_row + i * kPerWarp;
+          const float up = qrow < rows ? copysignf(__uint_as_float((uint32_t)(127 + 10 - e) << 23), a.scale_log2) : 0.f;
           uint4 o;
           o.x = pack2(f0.x * up, f2.x * up), o.y = pack2(f0.y * up, f2.y * up);
           o.z = pack2(f1.x * up, f3.x * up), o.w = pack2(f1.y * up, f3.y * up);
-          *reinterpret_cast<uint4*>(smem + C::kQ + t * C::kTileBytes + (i >> 3) * 16384 + tr * 128 +
-                                    (((i & 7) ^ (tr & 7)) << 4)) = o;
+          const int in_tile = qrow - t * kTileRows;
+          *reinterpret_cast<uint4*>(smem + C::kQ + t * C::kTileBytes + (part8 >> 3) * 16384 + in_tile * 128 +
+                                    (((part8 & 7) ^ (in_tile & 7)) << 4)) = o;
+          // lane x of the warp owns row x: its exponent lies with the lanes of that row
+          const int theirs = __shfl_sync(0xffffffffu, e, (lane % kPerWarp) * kLanes);
+          if (lane / kPerWarp == i) my_e = theirs;
         }
+        const float kappa = fmaxf(__uint_as_float((uint32_t)(127 - 10 + my_e) << 23) * fabsf(a.scale_log2), 1e-37f);
         fence_async_smem();
         tc_before();
         mbar_arrive(&ctl.q_full[t]);
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         n_o++;
         tc_after();
         const bool all = s0 == 0 && s1 == it.steps;
-        float* part = pa.parts + (size_t)(2 * blockIdx.x + (range.u0 > at ? 0 : 1)) * C::kPartFloats;
+        float* part = pa.parts + (size_t)(2 * blockIdx.x + (s0 > 0 ? 0 : 1)) * C::kPartFloats;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
         T* out = static_cast<T*>(a.out) +
                  ((size_t)(it.seq.q0 + rr / a.group) * a.h_q + it.g * a.group + rr % a.group) * D;
@@ -442,23 +452,23 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         if (!all && s0 == 0 && tid == 0) {
           KvpShared d;
           d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
-          d.parts = kvp_sharers(range, at + it.steps);
+          d.parts = kvp_sharers(range, it.end(at));
           d.pad[0] = d.pad[1] = d.pad[2] = 0;
           pa.desc[blockIdx.x] = d;
         }
       }
       step_no += s1 - s0;
-      if (at + it.steps >= range.u1) break;
-      at += it.steps;
-      it.next(a);
+      if (it.end(at) >= range.u1) break;
     }
   } else if (warp < kSoftWarps + kFillWarps) {
     regs_down<kFillRegs>();
     // ======================= decoding: a token per thread =====================
     const int fw = warp - kSoftWarps, tk = fw * 32 + lane, sub = tk >> 4, tt = tk & 15;
     uint4 kc[G], vc[G], kz, vz[G / 2];
-    for (;;) {
-      const int s0 = (int)(max(range.u0, at) - at), s1 = (int)(min(range.u1, at + it.steps) - at);
+    for (;; at = it.end(at), it.next(a)) {
+      const int2 my = it.part(at, range.u0, range.u1);
+      const int s0 = my.x, s1 = my.y;
+      if (s0 == s1) break;
       const int32_t* pages = a.pages + (long)it.b * a.max_pages;
       // the page entry of this thread's cache tile of a step (-1: none), and the tile's address
       auto entry = [&](int step) {
@@ -477,13 +487,13 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
       auto load_k = [&](const uint8_t* p) {
 #pragma unroll
         for (int g = 0; g < G; g++)
-          kc[g] = p ? __ldg(reinterpret_cast<const uint4*>(p + L::kKeyCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
+          kc[g] = p ? __ldcg(reinterpret_cast<const uint4*>(p + L::kKeyCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
         kz = make_uint4(0, 0, 0, 0);
         if (p) {
           if constexpr (G == 4) {
-            kz = __ldg(reinterpret_cast<const uint4*>(p + L::kKeyGrid + tt * 16));
+            kz = __ldcg(reinterpret_cast<const uint4*>(p + L::kKeyGrid + tt * 16));
           } else {
-            const uint2 z = __ldg(reinterpret_cast<const uint2*>(p + L::kKeyGrid + tt * 8));
+            const uint2 z = __ldcg(reinterpret_cast<const uint2*>(p + L::kKeyGrid + tt * 8));
             kz.x = z.x, kz.y = z.y;
           }
         }
@@ -491,10 +501,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
       auto load_v = [&](const uint8_t* p) {
 #pragma unroll
         for (int g = 0; g < G; g++)
-          vc[g] = p ? __ldg(reinterpret_cast<const uint4*>(p + L::kValueCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
+          vc[g] = p ? __ldcg(reinterpret_cast<const uint4*>(p + L::kValueCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int g = 0; g < G / 2; g++)
-          vz[g] = p ? __ldg(reinterpret_cast<const uint4*>(p + L::kValueGrid + (tt >> 1) * (8 * G) + g * 16))
+          vz[g] = p ? __ldcg(reinterpret_cast<const uint4*>(p + L::kValueGrid + (tt >> 1) * (8 * G) + g * 16))
                     : make_uint4(0, 0, 0, 0);
       };
       auto put = [&](uint8_t* dst, int g, const uint4& codes, __half2 s, __half2 m) {
@@ -546,9 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         tile = next;
       }
       step_no += s1 - s0;
-      if (at + it.steps >= range.u1) break;
-      at += it.steps;
-      it.next(a);
+      if (it.end(at) >= range.u1) break;
     }
   } else {
     regs_down<kIssueRegs>();
@@ -556,8 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
     if (warp == kSoftWarps + kFillWarps) {
       constexpr uint32_t kS = mma_desc(kTokens, false), kO = mma_desc(D, true);
       int n_q[2] = {0, 0}, n_p[2] = {0, 0};  // phases of q_full, p_full
-      for (;;) {
-        const int s0 = (int)(max(range.u0, at) - at), s1 = (int)(min(range.u1, at + it.steps) - at);
+      for (;; at = it.end(at), it.next(a)) {
+        const int2 my = it.part(at, range.u0, range.u1);
+        const int s0 = my.x, s1 = my.y;
+        if (s0 == s1) break;
         const int tiles = it.seq.n * a.group - it.rt * kRows > kTileRows ? 2 : 1;
         for (int j = s0; j <= s1; j++) {
           const int no = step_no + j - s0, st = no & 1;
@@ -601,9 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
           }
         }
         step_no += s1 - s0;
-        if (at + it.steps >= range.u1) break;
-        at += it.steps;
-        it.next(a);
+        if (it.end(at) >= range.u1) break;
       }
       if (elect_one()) tc_commit(&ctl.last);  // nothing is in flight when TMEM is given back
       __syncwarp();
