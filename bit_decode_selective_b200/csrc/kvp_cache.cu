@@ -59,6 +59,13 @@ __device__ __forceinline__ float tame(float x) {
   return isnan(x) ? 0.f : fminf(fmaxf(x, -kKvpLimit), kKvpLimit);
 }
 
+// The smaller of two values, a NaN if either is one.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The step of a group whose values span lo .. hi, fp16((hi - lo) / 15) in one
 // rounding from fp64.  In fp32 the quotient is within 2^-22 of itself of the
 // fp64 one; where that could round to another fp16 it is taken in fp64.
@@ -70,24 +77,38 @@ __device__ __forceinline__ uint16_t step16(float lo, float hi) {
 }
 
 // The codes of 8 values as a word, floor((v - m) / s + 1/2) clamped to 0 .. 15
-// as fp64 arithmetic decides.  fp32 finds (v - m) / s < 24 to 2^-22 of itself,
-// 6e-6: only values closer than 2e-5 to a border are decided in fp64.
+// as fp64 arithmetic decides.  fp32 finds 15 x, x = (v - m) / (15 s) saturated to
+// [0, 1], to 3e-6 and rounds it to the nearest integer by adding 1.5 * 2^23, which
+// leaves the code in the low mantissa bits.  Where some value is closer than 2e-5
+// to a half (bf16 values are on a coarse grid: one word in 170) the side of the
+// half is the sign of v - m - (k + 1/2) s, which a fused multiply-add gets right
+// where v - m is exact; where it is not, fp64 decides.
 __device__ __forceinline__ uint32_t codes8(const float (&v)[8], uint16_t s16, uint16_t m16) {
   if (s16 == 0) return 0u;
-  const float m = h2f(m16), inv = __frcp_rn(h2f(s16));
+  constexpr float kMagic = 12582912.f;
+  const float m = h2f(m16), s = h2f(s16), inv = __frcp_rn(15.f * s);
   uint32_t word = 0;
-  bool near_border = false;
+  bool near_half = false;
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const float u = fmaf(v[i] - m, inv, 0.5f);
-    // rounding down at 2^23 leaves floor(u) in the mantissa
-    const float c = fminf(fmaxf(u, 0.f), 15.5f);
-    const float r = __fadd_rd(c, 8388608.f);
-    const float frac = u - (r - 8388608.f);  // outside [0, 1) only where c was clamped
-    near_border = near_border || fabsf(frac) < 2e-5f || fabsf(frac - 1.f) < 2e-5f;
-    word |= (__float_as_uint(r) & 15u) << (4 * i);
+    const float x = __saturatef((v[i] - m) * inv);
+    const float r = fmaf(x, 15.f, kMagic);
+    near_half = near_half || fabsf(fmaf(x, 15.f, kMagic - r)) > 0.49998f;
+    word += (__float_as_uint(r) - 0x4B400000u) << (4 * i);
   }
-  if (near_border) {
+  if (!near_half) return word;
+  word = 0;
+  bool inexact = false;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float t = v[i] - m, back = t - v[i];
+    inexact = inexact || (v[i] - (t - back)) - (m + back) != 0.f;
+    const float x = __saturatef(t * inv), q = fmaf(x, 15.f, kMagic) - kMagic;
+    const float half = fmaf(x, 15.f, -q) >= 0.f ? q + 0.5f : q - 0.5f;
+    const float code = fmaf(-half, s, t) >= 0.f ? half + 0.5f : half - 0.5f;
+    word |= (__float_as_uint(fminf(code, 15.f) + kMagic) & 15u) << (4 * i);
+  }
+  if (inexact) {
     Grid16 g;
     g.s16 = s16, g.m16 = m16, g.S = h2d(s16), g.M = h2d(m16);
     word = 0;
@@ -159,13 +180,10 @@ __global__ void __launch_bounds__(kThreads) kvp_write_kernel(const __grid_consta
   uint32_t grid = 0;  // (s, m) of group c, or of group c % 2 where there are two
 #pragma unroll
   for (int g = 0; g < G; g++) {
-    float lo = v[g][0], hi = v[g][0], odd = 0.f;
+    float lo = v[g][0], hi = v[g][0];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      lo = fminf(lo, v[g][i]), hi = fmaxf(hi, v[g][i]);
-      odd = fmaf(v[g][i], 0.f, odd);  // NaN if some value is not finite
-    }
-    if (!(odd == 0.f) || lo < -kKvpLimit || hi > kKvpLimit) {
+    for (int i = 1; i < 8; i++) lo = min_nan(lo, v[g][i]), hi = fmaxf(hi, v[g][i]);
+    if (!(lo >= -kKvpLimit && hi <= kKvpLimit)) {  // a NaN makes lo one
       lo = INFINITY, hi = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
