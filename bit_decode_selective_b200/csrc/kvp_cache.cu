@@ -156,7 +156,7 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
 
 // blockIdx: (64 tokens, head, keys or values).
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) kvp_write_kernel(const __grid_constant__ CacheArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) kvp_write_kernel(const __grid_constant__ CacheArgs a) {
   using L = KvpTile<D>;
   constexpr int G = L::G;
   pdl_trigger();
