@@ -61,8 +61,9 @@ struct DecodeArgs {
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(fill ? 16 : 0) : "memory");
+// 16 bytes, of which the last 16 - bytes are zeros.
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(gmem), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -92,6 +93,13 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The first product of a sum: nothing to add to.
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -114,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   const KvpAttendArgs& a = da.a;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ KvpRangeShared range_sh;
-  __shared__ int tile_base[kWarps][C::kStages][kStepTiles];  // first token of a staged tile, -1: none
+  // first token of a staged tile, low bit: all rows see all of it; negative: nothing there
+  __shared__ __align__(8) int place[kWarps][C::kStages][kStepTiles];
   __shared__ float2 ml[kWarps][C::kRows];
   pdl_trigger();
   pdl_wait();
@@ -228,71 +237,71 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
       ref[nt][0] = ref[nt][1] = -INFINITY;
     }
 
-    // ---- the warp's steps s0 + warp, + kWarps, ...: page indices 32 steps ahead
+    // ---- the warp's steps s0 + warp, + kWarps, ...: lane l looks 32 steps
+    // ahead for the place in the pool (in tiles) and in the sequence of its step's tiles
     const int my_steps = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
-    int pg[kStepTiles];
-    auto load_pages = [&](int k0) {  // lane l: the tiles of the warp's step k0 + l
+    uint32_t at_pool[kStepTiles];
+    int at_seq[kStepTiles];
+    auto look = [&](int k0) {
       const int step = s0 + warp + (k0 + lane) * kWarps;
 #pragma unroll
       for (int j = 0; j < kStepTiles; j++) {
         const int i = step * kStepTiles + j;
-        pg[j] = -1;
+        at_pool[j] = 0, at_seq[j] = -16;
         if (k0 + lane < my_steps && i < it.span.tiles) {
-          const int page = pages[it.span.tile(i) >> (a.page_shift - 4)];
-          if (page >= 0 && page < a.n_pages)
-            pg[j] = page;
-          else
+          const int t = it.span.tile(i), page = pages[t >> (a.page_shift - 4)];
+          if (page >= 0 && page < a.n_pages) {
+            at_pool[j] = ((uint32_t)(page * a.h_kv + it.g) << (a.page_shift - 4)) + (t & ((1 << (a.page_shift - 4)) - 1));
+            at_seq[j] = t * 16 | (kvp_sees_all(a, it.span.p0, it.span.p1, t * 16, 16) ? 1 : 0);
+          } else {
             kvp_note_bad(a.bad);
+          }
         }
       }
     };
-    auto fetch = [&](int k) {  // copy the tiles of the warp's step k into its stage
+    int put_st = 0;
+    auto fetch = [&](int k) {  // copy the tiles of the warp's step k into the next stage
       if (k < my_steps) {
-        if ((k & 31) == 0) load_pages(k);
-        const int st = k % C::kStages;
-        const uint32_t dst = stage0_u + st * C::kStageBytes + lane * 16;
-        const int i0 = (s0 + warp + k * kWarps) * kStepTiles;
+        if ((k & 31) == 0) look(k);
+        const uint32_t dst = stage0_u + put_st * C::kStageBytes + lane * 16;
         const uint8_t* src[kStepTiles];
-        bool ok[kStepTiles];
+        int where[kStepTiles], bytes[kStepTiles];
 #pragma unroll
         for (int j = 0; j < kStepTiles; j++) {
-          const int page = __shfl_sync(0xffffffffu, pg[j], k & 31);
-          const int t = it.span.tile(i0 + j);
-          ok[j] = page >= 0;
-          const int in_page = t & ((1 << (a.page_shift - 4)) - 1);
-          src[j] = a.pool + ((((size_t)max(page, 0) * a.h_kv + it.g) << (a.page_shift - 4)) + in_page) * L::kBytes +
-                   lane * 16;
-          if (lane == 0) tile_base[warp][st][j] = ok[j] ? t * 16 : -1;
+          src[j] = a.pool + (size_t)__shfl_sync(0xffffffffu, at_pool[j], k & 31) * L::kBytes + lane * 16;
+          where[j] = __shfl_sync(0xffffffffu, at_seq[j], k & 31);
+          bytes[j] = where[j] >= 0 ? 16 : 0;  // nothing there: zeros
         }
+        if (lane == 0) *reinterpret_cast<int2*>(&place[warp][put_st][0]) = make_int2(where[0], where[1]);
         constexpr int kChunks = L::kBytes / 16;  // 16-byte pieces per tile: 160 or 80
 #pragma unroll
         for (int i = 0; i < kStepTiles * kChunks / 32; i++) {
-          const int piece = lane + 32 * i;
-          const bool second = piece >= kChunks;
-          const uint8_t* from = second ? src[1] + (32 * i - kChunks) * 16 : src[0] + 32 * i * 16;
-          cp_async16(dst + 32 * i * 16, from, second ? ok[1] : ok[0]);
+          const bool second = lane + 32 * i >= kChunks;
+          cp_async16(dst + 32 * i * 16, second ? src[1] + (32 * i - kChunks) * 16 : src[0] + 32 * i * 16,
+                     second ? bytes[1] : bytes[0]);
         }
+        if (++put_st == C::kStages) put_st = 0;
       }
       cp_commit();
     };
 #pragma unroll
     for (int k = 0; k < C::kStages - 1; k++) fetch(k);
 
+    int st = 0;
     for (int k = 0; k < my_steps; k++) {
       cp_wait<C::kStages - 2>();
-      __syncwarp();
-      const int st = k % C::kStages;
+      __syncwarp();  // the step's tiles are there, and the stage of the step before is free
+      fetch(k + C::kStages - 1);
       const uint32_t sb = stage0_u + st * C::kStageBytes;
       const uint8_t* sp = stage0 + st * C::kStageBytes;
 
       // ---- logits (log2 units): tokens gid, gid + 8 of each tile, rows 8 nt + 2 c, + 1
       float x[kStepTiles][NT][4];
-      int tb[kStepTiles];
-      bool whole = true;
+      const int2 pl = *reinterpret_cast<const int2*>(&place[warp][st][0]);
+      const int tb[kStepTiles] = {pl.x & ~1, pl.y & ~1};
+      const bool whole = pl.x & pl.y & 1;
 #pragma unroll
       for (int j = 0; j < kStepTiles; j++) {
-        tb[j] = tile_base[warp][st][j];
-        whole = whole && tb[j] >= 0 && kvp_sees_all(a, it.span.p0, it.span.p1, tb[j], 16);
         const uint32_t tile = sb + j * L::kBytes;
         const uint8_t* tp = sp + j * L::kBytes;
         // the token's steps, and its grid as an operand
@@ -315,11 +324,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
         }
         float xm[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-#pragma unroll
-          for (int e = 0; e < 4; e++) xm[nt][e] = 0.f, x[j][nt][e] = 0.f;
-          mma(xm[nt], za[0], za[1], za[0], za[1], qm[nt][0], qm[nt][1]);
-        }
+        for (int nt = 0; nt < NT; nt++) mma0(xm[nt], za[0], za[1], za[0], za[1], qm[nt][0], qm[nt][1]);
 #pragma unroll
         for (int g2 = 0; g2 < G; g2 += 2) {
           uint32_t w[4];  // [group g2: tokens 0..7, 8..15; group g2 + 1: ...]
@@ -333,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
                                  {v0 & 0x000F000Fu, v1 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x00F000F0u}};
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-              float acc[4] = {0.f, 0.f, 0.f, 0.f};
+              float acc[4];
 #pragma unroll
               for (int ks = 0; ks < 2; ks++) {
                 uint32_t q0, q1;
@@ -343,10 +348,14 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
                 } else {
                   q0 = qf[grp][ks][0], q1 = qf[grp][ks][1];
                 }
-                mma(acc, fa[ks][0], fa[ks][1], fa[ks][2], fa[ks][3], q0, q1);
+                if (ks == 0)
+                  mma0(acc, fa[ks][0], fa[ks][1], fa[ks][2], fa[ks][3], q0, q1);
+                else
+                  mma(acc, fa[ks][0], fa[ks][1], fa[ks][2], fa[ks][3], q0, q1);
               }
 #pragma unroll
-              for (int e = 0; e < 4; e++) x[j][nt][e] = fmaf(s[e >> 1][grp], acc[e], x[j][nt][e]);
+              for (int e = 0; e < 4; e++)
+                x[j][nt][e] = grp == 0 ? s[e >> 1][grp] * acc[e] : fmaf(s[e >> 1][grp], acc[e], x[j][nt][e]);
             }
           }
         }
@@ -461,8 +470,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
           }
         }
       }
-      __syncwarp();  // the stage is free
-      fetch(k + C::kStages - 1);
+      if (++st == C::kStages) st = 0;
     }
 
     // ---- join the warps
