@@ -76,6 +76,7 @@ extern "C" sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_ro
   while ((1 << a.page_shift) < kv->page) a.page_shift++;
   a.n_q = n_q, a.batch = batch, a.max_pages = max_pages, a.sinks = sinks;
   a.window = window < (long long)max_pages * kv->page ? window : 0;  // as wide as any sequence: no window
+  kvp_divisor((uint32_t)a.group, a.group_mul, a.group_shift);
   a.scale_log2 = (float)((double)scale * 1.4426950408889634);
   a.few_rows = kFewRows;
   a.ws = ws;

@@ -17,6 +17,7 @@ struct KvpAttendArgs {
   int32_t* bad;
   int n_pages, page_shift, h_kv, h_q, group;  // group: query heads per KV head
   int n_q, batch, max_pages, window, sinks;   // window < max_pages * page, 0: none
+  uint32_t group_mul, group_shift;            // n / group = n * group_mul >> group_shift, 0 <= n < 2^31
   float scale_log2;                           // scale * log2(e)
   int few_rows;                               // sequences of at most this many rows are the few-row kernel's
   void* ws;
@@ -41,6 +42,17 @@ sf_status launch_kvp_decode(const KvpAttendArgs& a, int d, sf_dtype dtype, int r
 // Many-row kernel (kvp_prefill.cu).
 size_t kvp_prefill_workspace(int d);
 sf_status launch_kvp_prefill(const KvpAttendArgs& a, int d, sf_dtype dtype, cudaStream_t s);
+
+// The multiplier and shift of a division by d >= 1: with 2^(s-1) < d <= 2^s,
+// ceil(2^(31+s) / d) is below 2^32 and exact for numerators below 2^31.
+inline void kvp_divisor(uint32_t d, uint32_t& mul, uint32_t& shift) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) s++;
+  mul = (uint32_t)(((1ull << (31 + s)) + d - 1) / d), shift = 31 + s;
+}
+__device__ __forceinline__ int kvp_by_group(const KvpAttendArgs& a, int n) {
+  return (int)((uint64_t)(uint32_t)n * a.group_mul >> a.group_shift);
+}
 
 __device__ __forceinline__ void kvp_note_bad(int32_t* bad) {
   if (bad) atomicAdd(bad, 1);
@@ -109,16 +121,9 @@ struct KvpItem {
   }
   static __device__ __forceinline__ KvpSpan span_of(const KvpAttendArgs& a, const KvpSeq& s, int rt) {
     const int last = min((rt + 1) * ROWS, s.n * a.group) - 1;
-    return kvp_span(a, s.len - s.n + rt * ROWS / a.group, s.len - s.n + last / a.group);
+    return kvp_span(a, s.len - s.n + kvp_by_group(a, rt * ROWS), s.len - s.n + kvp_by_group(a, last));
   }
   static __device__ __forceinline__ int steps_of(const KvpSpan& s) { return max(1, (s.tiles + STEP - 1) / STEP); }
-  // Steps of one sequence, over its row tiles (not yet times the KV heads).
-  static __device__ __forceinline__ long seq_steps(const KvpAttendArgs& a, const KvpSeq& s) {
-    const int n = row_tiles(a, s);
-    long sum = 0;
-    for (int rt = 0; rt < n; rt++) sum += EXTRA + steps_of(span_of(a, s, rt));
-    return sum;
-  }
   // The end of the item that starts at `at`, and the steps of it [s0, s1) that
   // lie in [u0, u1) (none: s0 == s1).
   __device__ __forceinline__ long end(long at) const { return at + EXTRA + steps; }
@@ -142,24 +147,48 @@ struct KvpItem {
   }
 };
 
-// This CTA's range [u0, u1) of the line (u0 == u1: nothing), and the item and
-// place `at` on the line where it starts.  All threads call it.
+// This CTA's range [u0, u1) of the line (u0 == u1: nothing), and the place `at`
+// on the line of the item where it starts.  The first `more` ranges have size
+// `each` + 1, the others `each`.  The line is counted in 64 bits, but divided in 32:
+// a line past 2^32 steps is cut in larger units.
 struct KvpRange {
-  long u0, u1, at, total, ctas;
+  long u0, u1, at;
+  uint32_t each, more;
+  int unit;
+  __device__ __forceinline__ long begin(uint32_t cta) const {
+    return ((long)cta * each + min(cta, more)) << unit;
+  }
+  // the CTA whose range holds step u of the line
+  __device__ __forceinline__ uint32_t cta_of(long u) const {
+    const uint32_t x = (uint32_t)(u >> unit), big = more * (each + 1);
+    return x < big ? x / (each + 1) : more + (x - big) / each;
+  }
 };
+template <typename Item>
 struct KvpRangeShared {
   long scan[32];
   long at;
-  int b, rt, g;
+  Item it;
 };
-template <int THREADS, typename Item>
-__device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_steps, KvpRangeShared& sh, Item& it) {
+// All threads of the CTA call it, the work of the sequences split over them:
+// thread by thread, or with SPREAD warp by warp, the lanes over the row tiles of
+// long queries.  `it` is set where the range is not empty.
+template <int THREADS, bool SPREAD, typename Item>
+__device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_steps, KvpRangeShared<Item>& sh, Item& it) {
+  constexpr int kParts = SPREAD ? THREADS / 32 : THREADS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int me = SPREAD ? warp : tid;
+  const int per = (a.batch + kParts - 1) / kParts;
+  const int b0 = min(me * per, a.batch), b1 = min(b0 + per, a.batch);
+  // steps of my sequences' items; SPREAD: of my lane's row tiles
   long mine = 0;
-  const int per = (a.batch + THREADS - 1) / THREADS;
-  const int b0 = min(tid * per, a.batch), b1 = min(b0 + per, a.batch);
-  for (int b = b0; b < b1; b++) mine += Item::seq_steps(a, kvp_seq(a, b)) * a.h_kv;
-  long upto = mine;
+  for (int b = b0; b < b1; b++) {
+    const KvpSeq s = kvp_seq(a, b);
+    const int n = Item::row_tiles(a, s);
+    for (int rt = SPREAD ? lane : 0; rt < n; rt += SPREAD ? 32 : 1) mine += Item::kExtra + Item::steps_of(Item::span_of(a, s, rt));
+  }
+  mine *= a.h_kv;
+  long upto = mine;  // inclusive sum over the lanes
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -167,39 +196,65 @@ __device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_st
   }
   if (lane == 31) sh.scan[warp] = upto;
   __syncthreads();
-  KvpRange r;
-  r.total = 0;
+  long before = 0, total = 0;  // of the warps before this one, of all
 #pragma unroll
   for (int w = 0; w < THREADS / 32; w++) {
-    if (w < warp) upto += sh.scan[w];
-    r.total += sh.scan[w];
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
   }
-  r.ctas = min((long)gridDim.x, (r.total + min_steps - 1) / min_steps);
-  r.u0 = r.u1 = 0;
-  if ((long)blockIdx.x >= r.ctas) return r;  // all threads alike
-  r.u0 = r.total * blockIdx.x / r.ctas, r.u1 = r.total * (blockIdx.x + 1) / r.ctas;
-  if (r.u0 >= upto - mine && r.u0 < upto) {  // one thread
-    long at = upto - mine;
+  KvpRange r;
+  r.u0 = r.u1 = r.at = 0;
+  r.unit = 0;
+  while (total >> r.unit >> 32) r.unit++;
+  const uint32_t units = (uint32_t)((total + (1l << r.unit) - 1) >> r.unit);
+  const uint32_t ctas = min(gridDim.x, (units + min_steps - 1) / min_steps);
+  if (blockIdx.x >= ctas) return r;  // all threads alike
+  r.each = units / ctas, r.more = units - r.each * ctas;
+  r.u0 = r.begin(blockIdx.x), r.u1 = min(r.begin(blockIdx.x + 1), total);
+  if (r.u0 >= total) {  // (the last unit can be a short one)
+    r.u1 = r.u0;
+    return r;
+  }
+  // the part that holds u0 finds its item
+  const long from = SPREAD ? before : before + upto - mine, to = SPREAD ? before + sh.scan[warp] : before + upto;
+  if (r.u0 >= from && r.u0 < to) {
+    long at = from;
     bool found = false;
     for (int b = b0; b < b1 && !found; b++) {
       const KvpSeq s = kvp_seq(a, b);
       const int n = Item::row_tiles(a, s);
-      for (int rt = 0; rt < n && !found; rt++) {
-        const int st = Item::kExtra + Item::steps_of(Item::span_of(a, s, rt));
-        if (r.u0 < at + (long)st * a.h_kv) {
-          sh.b = b, sh.rt = rt, sh.g = (int)((r.u0 - at) / st);
-          sh.at = at + (long)sh.g * st;
-          found = true;
+      for (int rt0 = 0; rt0 < n && !found; rt0 += SPREAD ? 32 : 1) {
+        const int rt = rt0 + (SPREAD ? lane : 0);
+        const int st = rt < n ? Item::kExtra + Item::steps_of(Item::span_of(a, s, rt)) : 0;
+        const long all = (long)st * a.h_kv;
+        long end = all;  // inclusive sum over the row tiles at hand
+        if (SPREAD) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const long x = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += x;
+          }
+        }
+        const bool here = r.u0 >= at + end - all && r.u0 < at + end;
+        if (here) {
+          const int g = (int)((uint32_t)(r.u0 - (at + end - all)) / (uint32_t)st);
+          sh.it.b = b, sh.it.rt = rt, sh.it.g = g;
+          sh.it.seq = s;
+          sh.it.set(a);
+          sh.at = at + end - all + (long)g * st;
+        }
+        if (SPREAD) {
+          found = __any_sync(0xffffffffu, here);
+          at += __shfl_sync(0xffffffffu, end, 31);
         } else {
-          at += (long)st * a.h_kv;
+          found = here;
+          at += end;
         }
       }
     }
   }
   __syncthreads();
-  it.b = sh.b, it.rt = sh.rt, it.g = sh.g;
-  it.seq = kvp_seq(a, it.b);
-  it.set(a);
+  it = sh.it;
   r.at = sh.at;
   return r;
 }
@@ -207,15 +262,12 @@ __device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_st
 // An item that several CTAs share, written by the one with its first step.
 struct KvpShared {
   int q_row, row0, rows, head0;  // first query row of the sequence, first row, rows, first query head
-  int parts, pad[3];
+  int parts, cta, pad[2];       // CTAs that share it, the first of them
 };
 // How many CTAs share the item that ends at `end` and has its first step in
 // this one's range.
 __device__ __forceinline__ int kvp_sharers(const KvpRange& r, long end) {
-  long last = (end * r.ctas + r.total - 1) / r.total - 1;
-  while (r.total * (last + 1) / r.ctas < end) last++;
-  while (r.total * last / r.ctas >= end) last--;
-  return (int)(last - blockIdx.x + 1);
+  return (int)(r.cta_of(end - 1) - blockIdx.x + 1);
 }
 
 __device__ __forceinline__ bool kvp_sees(const KvpAttendArgs& a, int p, int j) {

@@ -57,7 +57,11 @@ struct Cfg {
 struct DecodeArgs {
   KvpAttendArgs a;
   float* parts;     // [2 * ctas][part floats]
-  KvpShared* desc;  // [ctas]
+  // an item's entry: at (item number), written by the CTA with its first step,
+  // where every item has one (no cu_q) and they are fewer than the CTAs; else at
+  // that CTA, each CTA clearing its own before it starts
+  KvpShared* desc;
+  int by_item;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   constexpr int G = L::G, MT = D / 16;
   const KvpAttendArgs& a = da.a;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ KvpRangeShared range_sh;
+  __shared__ KvpRangeShared<KvpItem<C::kRows, kStepTiles, kExtra, true>> range_sh;
   // first token of a staged tile, low bit: all rows see all of it; negative: nothing there
   __shared__ __align__(8) int place[kWarps][C::kStages][kStepTiles];
   __shared__ float2 ml[kWarps][C::kRows];
@@ -131,8 +135,8 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
   const int gid = lane >> 2, c = lane & 3;
 
   KvpItem<C::kRows, kStepTiles, kExtra, true> it;
-  const KvpRange range = kvp_range<kThreads>(a, kWarps, range_sh, it);  // at least a step per warp
-  if (tid == 0) da.desc[blockIdx.x].parts = 0;
+  const KvpRange range = kvp_range<kThreads, false>(a, kWarps, range_sh, it);  // at least a step per warp
+  if (tid == 0 && !da.by_item) da.desc[blockIdx.x].parts = 0;
   if (range.u0 == range.u1) return;
   const long u0 = range.u0, u1 = range.u1;
   long at = range.at;
@@ -149,6 +153,56 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
     const int base = it.seq.len - it.seq.n, row0 = it.rt * C::kRows;
     const int32_t* pages = a.pages + (long)it.b * a.max_pages;
 
+    // ---- the warp's steps s0 + warp, + kWarps, ...: lane l looks 32 steps
+    // ahead for the place in the pool (in tiles) and in the sequence of its step's tiles
+    const int my_steps = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
+    uint32_t at_pool[kStepTiles];
+    int at_seq[kStepTiles];
+    auto look = [&](int k0) {
+      const int step = s0 + warp + (k0 + lane) * kWarps;
+#pragma unroll
+      for (int j = 0; j < kStepTiles; j++) {
+        const int i = step * kStepTiles + j;
+        at_pool[j] = 0, at_seq[j] = -16;
+        if (k0 + lane < my_steps && i < it.span.tiles) {
+          const int t = it.span.tile(i), page = pages[t >> (a.page_shift - 4)];
+          if (page >= 0 && page < a.n_pages) {
+            at_pool[j] = ((uint32_t)(page * a.h_kv + it.g) << (a.page_shift - 4)) + (t & ((1 << (a.page_shift - 4)) - 1));
+            at_seq[j] = t * 16 | (kvp_sees_all(a, it.span.p0, it.span.p1, t * 16, 16) ? 1 : 0);
+          } else {
+            kvp_note_bad(a.bad);
+          }
+        }
+      }
+    };
+    int put_st = 0;
+    auto fetch = [&](int k) {  // copy the tiles of the warp's step k into the next stage
+      if (k < my_steps) {
+        if ((k & 31) == 0) look(k);
+        const uint32_t dst = stage0_u + put_st * C::kStageBytes + lane * 16;
+        const uint8_t* src[kStepTiles];
+        int where[kStepTiles], bytes[kStepTiles];
+#pragma unroll
+        for (int j = 0; j < kStepTiles; j++) {
+          src[j] = a.pool + (size_t)__shfl_sync(0xffffffffu, at_pool[j], k & 31) * L::kBytes + lane * 16;
+          where[j] = __shfl_sync(0xffffffffu, at_seq[j], k & 31);
+          bytes[j] = where[j] >= 0 ? 16 : 0;  // nothing there: zeros
+        }
+        if (lane == 0) *reinterpret_cast<int2*>(&place[warp][put_st][0]) = make_int2(where[0], where[1]);
+        constexpr int kChunks = L::kBytes / 16;  // 16-byte pieces per tile: 160 or 80
+#pragma unroll
+        for (int i = 0; i < kStepTiles * kChunks / 32; i++) {
+          const bool second = lane + 32 * i >= kChunks;
+          cp_async16(dst + 32 * i * 16, second ? src[1] + (32 * i - kChunks) * 16 : src[0] + 32 * i * 16,
+                     second ? bytes[1] : bytes[0]);
+        }
+        if (++put_st == C::kStages) put_st = 0;
+      }
+      cp_commit();
+    };
+#pragma unroll
+    for (int k = 0; k < C::kStages - 1; k++) fetch(k);
+
     // ---- query operands.  Row 8 nt + gid: this lane's elements 32 grp + 8 c + (0..7)
     uint32_t qf[NT > 1 ? 1 : G][2][2];  // [group][k-step][b0, b1]
     uint32_t qm[NT][2];                 // sums over group c, high and low part
@@ -160,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
       float v[G][8];
       float top = 0.f;
       if (r < rows) {
-        const int i = (row0 + r) / a.group, h = it.g * a.group + (row0 + r) % a.group;
+        const int i = kvp_by_group(a, row0 + r), h = it.g * a.group + row0 + r - kvp_by_group(a, row0 + r) * a.group;
         const T* qr = static_cast<const T*>(a.q) + (it.seq.q0 + i) * a.q_row + h * a.q_head + 8 * c;
 #pragma unroll
         for (int grp = 0; grp < G; grp++) {
@@ -221,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
         const float back = __uint_as_float((uint32_t)(127 - 10 + er) << 23) * a.scale_log2;
         k1[nt][k] = back * 16777216.f, k2[nt][k] = back * 4.f;
         const int rr = min(8 * nt + 2 * c + k, rows - 1);
-        pos[nt][k] = base + (row0 + rr) / a.group;
+        pos[nt][k] = base + kvp_by_group(a, row0 + rr);
       }
     }
     if constexpr (NT > 1) __syncthreads();
@@ -236,56 +290,6 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
       lsum[nt][0] = lsum[nt][1] = 0.f;
       ref[nt][0] = ref[nt][1] = -INFINITY;
     }
-
-    // ---- the warp's steps s0 + warp, + kWarps, ...: lane l looks 32 steps
-    // ahead for the place in the pool (in tiles) and in the sequence of its step's tiles
-    const int my_steps = s1 - s0 > warp ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;
-    uint32_t at_pool[kStepTiles];
-    int at_seq[kStepTiles];
-    auto look = [&](int k0) {
-      const int step = s0 + warp + (k0 + lane) * kWarps;
-#pragma unroll
-      for (int j = 0; j < kStepTiles; j++) {
-        const int i = step * kStepTiles + j;
-        at_pool[j] = 0, at_seq[j] = -16;
-        if (k0 + lane < my_steps && i < it.span.tiles) {
-          const int t = it.span.tile(i), page = pages[t >> (a.page_shift - 4)];
-          if (page >= 0 && page < a.n_pages) {
-            at_pool[j] = ((uint32_t)(page * a.h_kv + it.g) << (a.page_shift - 4)) + (t & ((1 << (a.page_shift - 4)) - 1));
-            at_seq[j] = t * 16 | (kvp_sees_all(a, it.span.p0, it.span.p1, t * 16, 16) ? 1 : 0);
-          } else {
-            kvp_note_bad(a.bad);
-          }
-        }
-      }
-    };
-    int put_st = 0;
-    auto fetch = [&](int k) {  // copy the tiles of the warp's step k into the next stage
-      if (k < my_steps) {
-        if ((k & 31) == 0) look(k);
-        const uint32_t dst = stage0_u + put_st * C::kStageBytes + lane * 16;
-        const uint8_t* src[kStepTiles];
-        int where[kStepTiles], bytes[kStepTiles];
-#pragma unroll
-        for (int j = 0; j < kStepTiles; j++) {
-          src[j] = a.pool + (size_t)__shfl_sync(0xffffffffu, at_pool[j], k & 31) * L::kBytes + lane * 16;
-          where[j] = __shfl_sync(0xffffffffu, at_seq[j], k & 31);
-          bytes[j] = where[j] >= 0 ? 16 : 0;  // nothing there: zeros
-        }
-        if (lane == 0) *reinterpret_cast<int2*>(&place[warp][put_st][0]) = make_int2(where[0], where[1]);
-        constexpr int kChunks = L::kBytes / 16;  // 16-byte pieces per tile: 160 or 80
-#pragma unroll
-        for (int i = 0; i < kStepTiles * kChunks / 32; i++) {
-          const bool second = lane + 32 * i >= kChunks;
-          cp_async16(dst + 32 * i * 16, second ? src[1] + (32 * i - kChunks) * 16 : src[0] + 32 * i * 16,
-                     second ? bytes[1] : bytes[0]);
-        }
-        if (++put_st == C::kStages) put_st = 0;
-      }
-      cp_commit();
-    };
-#pragma unroll
-    for (int k = 0; k < C::kStages - 1; k++) fetch(k);
 
     int st = 0;
     for (int k = 0; k < my_steps; k++) {
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
       }
       if (all) {
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
-        const int qi = (row0 + r) / a.group, h = it.g * a.group + (row0 + r) % a.group;
+        const int qi = kvp_by_group(a, row0 + r), h = it.g * a.group + row0 + r - kvp_by_group(a, row0 + r) * a.group;
         T* out = static_cast<T*>(a.out) + ((size_t)(it.seq.q0 + qi) * a.h_q + h) * D + d4;
         *reinterpret_cast<uint2*>(out) =
             make_uint2(Elem<T>::from_float2(sum.x * inv, sum.y * inv), Elem<T>::from_float2(sum.z * inv, sum.w * inv));
@@ -522,82 +526,99 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(c
         if (d4 == 0) *reinterpret_cast<float2*>(part + C::kRows * D + 2 * r) = make_float2(top, l);
       }
     }
-    // the CTA with the item's start tells the merge kernel how many share it
-    if (!all && s0 == 0 && tid == 0) {
+    // the CTA with the item's first step tells the merge kernel how many share it
+    if (s0 == 0 && tid == 0 && (!all || da.by_item)) {
       KvpShared d;
       d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
-      d.parts = kvp_sharers(range, it.end(at));
-      d.pad[0] = d.pad[1] = d.pad[2] = 0;
-      da.desc[blockIdx.x] = d;
+      d.parts = all ? 0 : kvp_sharers(range, it.end(at));
+      d.cta = blockIdx.x;
+      d.pad[0] = d.pad[1] = 0;
+      da.desc[da.by_item ? (it.b * it.row_tiles(a, it.seq) + it.rt) * a.h_kv + it.g : blockIdx.x] = d;
     }
     __syncthreads();  // the exchange is read
     if (it.end(at) >= u1) break;
   }
 }
 
-// One CTA per (CTA of the pass, 4 rows): joins the parts of the item that
-// starts there and goes on into the ranges of the CTAs after it.  128 threads a
-// row: a thread sums 4 elements over every (512 / D)-th part, and the shares
-// are added in order.
-constexpr int kMergeRows = 4, kMergeThreads = 128 * kMergeRows;
+// Joins the parts of an item: those of the CTA that has its first step (its
+// second place) and of the CTAs after it (their first).  Part i goes to share i
+// mod 2048 / D, the shares are summed and then added in order, whatever the form:
+// a CTA takes ROWS rows of an item, 512 / ROWS threads a row, 4 elements and
+// ROWS shares a thread.  With few items each row has a CTA of its own, so that
+// its parts' loads are all under way at once.
+constexpr int kMergeThreads = 512;
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) kvp_merge_kernel(const __grid_constant__ DecodeArgs da) {
   using C = Cfg<D, NT>;
-  constexpr int kShares = 128 / (D / 4);
+  constexpr int kPer = kMergeThreads / ROWS, kShares = kMergeThreads / (D / 4), kThreadsPerElem = kPer / (D / 4);
   const KvpAttendArgs& a = da.a;
-  __shared__ float4 sums[kMergeRows][kShares][D / 4];
-  __shared__ float ls[kMergeRows][kShares], tops[kMergeRows][4];
+  __shared__ float4 sums[ROWS][kShares][D / 4];
+  __shared__ float2 ls[ROWS][kShares];  // reference, weight sum
   pdl_trigger();
   pdl_wait();
   const KvpShared d = da.desc[blockIdx.x];
-  const int rt = threadIdx.x >> 7, r = blockIdx.y * kMergeRows + rt, tid = threadIdx.x & 127;
+  const int rt = threadIdx.x / kPer, r = blockIdx.y * ROWS + rt, tid = threadIdx.x % kPer;
   if (d.parts == 0) return;
   const bool live = r < d.rows;
-  auto part = [&](int i) {  // the first lies in the starting CTA's second place, the others in their CTA's first
-    return da.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::kPartFloats;
-  };
-  float top = -INFINITY;
-  if (live)
-    for (int i = tid; i < d.parts; i += 128) top = fmaxf(top, part(i)[C::kRows * D + 2 * r]);
+  const int q4 = tid % (D / 4);
+#pragma unroll 1
+  for (int share = tid / (D / 4); share < min(kShares, d.parts); share += kThreadsPerElem) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f, top = -INFINITY;
+    if (live) {
+      constexpr int kAhead = 4;
+      for (int i0 = share; i0 < d.parts; i0 += kAhead * kShares) {
+        float2 m[kAhead];
+        float4 v[kAhead];
 #pragma unroll
-  for (int sh = 16; sh > 0; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
-  if ((tid & 31) == 0) tops[rt][tid >> 5] = top;
+        for (int k = 0; k < kAhead; k++) {
+          const int i = i0 + k * kShares;
+          m[k] = make_float2(-INFINITY, 0.f), v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < d.parts) {
+            const float* p = da.parts + (size_t)(2 * (d.cta + i) + (i == 0 ? 1 : 0)) * C::kPartFloats;
+            m[k] = *reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r);
+            v[k] = *reinterpret_cast<const float4*>(p + r * D + 4 * q4);
+          }
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) now = fmaxf(now, m[k].x);
+        const float old = top == -INFINITY ? 0.f : ex2(top - now);
+        sum.x *= old, sum.y *= old, sum.z *= old, sum.w *= old, l *= old;
+        top = now;
+#pragma unroll
+        for (int k = 0; k < kAhead; k++) {
+          const float f = m[k].x == -INFINITY ? 0.f : ex2(m[k].x - top);
+          sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
+          sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
+          l = fmaf(f, m[k].y, l);
+        }
+      }
+    }
+    sums[rt][share][q4] = sum;
+    if (q4 == 0) ls[rt][share] = make_float2(top, l);
+  }
   __syncthreads();
-  top = fmaxf(fmaxf(tops[rt][0], tops[rt][1]), fmaxf(tops[rt][2], tops[rt][3]));
-  const int share = tid / (D / 4), q4 = tid % (D / 4);
+  if (tid >= D / 4 || !live) return;
+  const int shares = min(kShares, d.parts);
+  float top = -INFINITY, l = 0.f;
+  for (int k = 0; k < shares; k++) top = fmaxf(top, ls[rt][k].x);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-  if (live) {
 #pragma unroll 4
-    for (int i = share; i < d.parts; i += kShares) {
-      const float* p = part(i);
-      const float2 m = *reinterpret_cast<const float2*>(p + C::kRows * D + 2 * r);
-      const float4 v = *reinterpret_cast<const float4*>(p + r * D + 4 * q4);
-      const float f = m.x == -INFINITY ? 0.f : ex2(m.x - top);
-      sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
-      sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
-      l = fmaf(f, m.y, l);
-    }
+  for (int k = 0; k < shares; k++) {
+    const float2 m = ls[rt][k];
+    const float f = m.x == -INFINITY ? 0.f : ex2(m.x - top);
+    const float4 v = sums[rt][k][q4];
+    sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
+    sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+    l = fmaf(f, m.y, l);
   }
-  sums[rt][share][q4] = sum;
-  if (q4 == 0) ls[rt][share] = l;
-  __syncthreads();
-  if (share == 0 && live) {
-    l = 0.f;
-#pragma unroll
-    for (int k = 0; k < kShares; k++) l += ls[rt][k];
-#pragma unroll
-    for (int k = 1; k < kShares; k++) {
-      const float4 v = sums[rt][k][q4];
-      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int qi = (d.row0 + r) / a.group, h = d.head0 + (d.row0 + r) % a.group;
-    T* out = static_cast<T*>(a.out) + ((size_t)(d.q_row + qi) * a.h_q + h) * D + 4 * q4;
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(Elem<T>::from_float2(sum.x * inv, sum.y * inv), Elem<T>::from_float2(sum.z * inv, sum.w * inv));
-  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int qi = kvp_by_group(a, d.row0 + r), h = d.head0 + d.row0 + r - qi * a.group;
+  T* out = static_cast<T*>(a.out) + ((size_t)(d.q_row + qi) * a.h_q + h) * D + 4 * q4;
+  *reinterpret_cast<uint2*>(out) =
+      make_uint2(Elem<T>::from_float2(sum.x * inv, sum.y * inv), Elem<T>::from_float2(sum.z * inv, sum.w * inv));
 }
 
 int row_blocks(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
@@ -611,12 +632,18 @@ sf_status launch_decode(const KvpAttendArgs& a, cudaStream_t s) {
   da.a = a;
   da.desc = static_cast<KvpShared*>(a.ws);
   da.parts = reinterpret_cast<float*>(da.desc + ctas);
+  // without cu_q the rows of every sequence, and so the items, are known
+  const long each = (long)(a.n_q / a.batch) * a.group;
+  const int most = a.cu_q ? C::kRows : (int)std::min<long>(each, C::kRows);
+  const long items = (each + C::kRows - 1) / C::kRows * a.h_kv * a.batch;
+  da.by_item = !a.cu_q && items < ctas;
+  const int entries = da.by_item ? (int)items : ctas;
   SF_CUDA((kvp_allow_smem<kvp_decode_kernel<T, D, NT>>(C::kSmem)));
   SF_CUDA(launch_pdl(kvp_decode_kernel<T, D, NT>, dim3(ctas), dim3(kThreads), C::kSmem, s, da));
-    // without cu_q the rows of every sequence are known
-  const int most = a.cu_q ? C::kRows : (int)std::min<long>((long)(a.n_q / a.batch) * a.group, C::kRows);
-  SF_CUDA(launch_pdl(kvp_merge_kernel<T, D, NT>, dim3(ctas, (most + kMergeRows - 1) / kMergeRows), dim3(kMergeThreads),
-                     0, s, da));
+  if ((long)entries * most <= 2l * num_sms())
+    SF_CUDA(launch_pdl(kvp_merge_kernel<T, D, NT, 1>, dim3(entries, most), dim3(kMergeThreads), 0, s, da));
+  else
+    SF_CUDA(launch_pdl(kvp_merge_kernel<T, D, NT, 4>, dim3(entries, (most + 3) / 4), dim3(kMergeThreads), 0, s, da));
   return SF_OK;
 }
 

@@ -233,7 +233,7 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, __half2 m) {
 struct Control {
   uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], last;
-  KvpRangeShared range;
+  KvpRangeShared<Item> range;
   // first token of each cache tile of the step, low bit: all rows see all of
   // it; -16: nothing there
   int place[kRing][kStep];
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
   }
   pdl_wait();
   Item it;
-  const KvpRange range = kvp_range<kThreads>(a, kMinSteps, ctl.range, it);
+  const KvpRange range = kvp_range<kThreads, true>(a, kMinSteps, ctl.range, it);
   if (tid == 0) pa.desc[blockIdx.x].parts = 0;
   if (range.u0 == range.u1) return;
   if (warp == kSoftWarps + kFillWarps) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
       const int row0 = it.rt * kRows, rows = min(it.seq.n * a.group - row0, kRows);
       if (t == 0 || rows > kTileRows) {
         const int rr = row0 + min(r, rows - 1);
-        const int pos = it.seq.len - it.seq.n + rr / a.group;
+        const int pos = it.seq.len - it.seq.n + kvp_by_group(a, rr);
         // ---- the tile's queries: D / 8 lanes a row, each row scaled by a power
         // of two into fp16's range.  A negative scale turns the query around and
         // a scale of 0 becomes one that rounds away, so that the largest S is
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         for (int i = 0; i < kLanes; i++) {
           const int x = row0 + min(first_row + i * kPerWarp, rows - 1);
           w[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                      (it.seq.q0 + x / a.group) * a.q_row +
-                                                      (it.g * a.group + x % a.group) * a.q_head) + part8);
+                                                      (it.seq.q0 + kvp_by_group(a, x)) * a.q_row +
+                                                      (it.g * a.group + x - kvp_by_group(a, x) * a.group) * a.q_head) + part8);
         }
         int my_e = 0;
 #pragma unroll
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         float* part = pa.parts + (size_t)(2 * blockIdx.x + (s0 > 0 ? 0 : 1)) * C::kPartFloats;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
         T* out = static_cast<T*>(a.out) +
-                 ((size_t)(it.seq.q0 + rr / a.group) * a.h_q + it.g * a.group + rr % a.group) * D;
+                 ((size_t)(it.seq.q0 + kvp_by_group(a, rr)) * a.h_q + it.g * a.group + rr - kvp_by_group(a, rr) * a.group) * D;
 #pragma unroll
         for (int ch = 0; ch < D / 32; ch++) {
           uint32_t o[32];
@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
           KvpShared d;
           d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
           d.parts = kvp_sharers(range, it.end(at));
-          d.pad[0] = d.pad[1] = d.pad[2] = 0;
+          d.cta = blockIdx.x;
+          d.pad[0] = d.pad[1] = 0;
           pa.desc[blockIdx.x] = d;
         }
       }
