@@ -10,9 +10,9 @@
 //                   TMEM, the weights go back into S's columns as the fp16
 //                   operand of the second product.  While one tile's weights
 //                   are made the tensor core works for the other.
-//   warps 8-11      decode 128 tokens' codes to fp16 keys and values in shared
+//   warps 8-15      decode 128 tokens' codes to fp16 keys and values in shared
 //                   memory (128-byte swizzle), once for both tiles
-//   warp 12         one thread issues the products
+//   warp 16         one thread issues the products
 // Numerics: keys and values are rounded once to fp16, as a 16-bit cache would
 // hold them; queries are scaled per row by a power of two into fp16's range
 // (exact for fp16 and bf16 but for elements 2^24 below the row's largest);
@@ -35,11 +35,11 @@ namespace {
 constexpr int kRows = 256, kTileRows = 128;
 constexpr int kStep = 8;                 // cache tiles per step: 128 tokens
 constexpr int kTokens = kStep * kKvpTile;
-constexpr int kSoftWarps = 8, kFillWarps = 4;
+constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kThreads = (kSoftWarps + kFillWarps + 4) * 32;  // the last warpgroup issues the products
-// registers per thread of the three kinds of warpgroup; together the 128 x 512
-// of the launch (65,536): 2 x 184 + 96 + 48 = 4 x 128
-constexpr int kSoftRegs = 184, kFillRegs = 96, kIssueRegs = 48;
+// Registers per thread: the launch's 96 x 640 threads = 480 x 128, given out anew
+// as (2 x 160 + 2 x 56 + 48) x 128.
+constexpr int kSoftRegs = 160, kFillRegs = 56, kIssueRegs = 48;
 constexpr int kRing = 4;                 // steps whose token places are kept
 constexpr float kRefGap = 6.f, kRefShift = 9.f;
 constexpr unsigned long long kWaitNs = 1000000000ull;  // bounded waits give up after 1 s
@@ -62,7 +62,11 @@ struct Cfg {
 struct PrefillArgs {
   KvpAttendArgs a;
   float* parts;     // [2 * ctas][part floats]
-  KvpShared* desc;  // [ctas]
+  // an item's entry: at (item number), written by the CTA with its first step,
+  // where every item has one (no cu_q) and they are fewer than the CTAs; else at
+  // that CTA, each CTA clearing its own before it starts
+  KvpShared* desc;
+  int by_item;
 };
 
 template <int N>
@@ -163,14 +167,32 @@ __device__ __forceinline__ void tc_ld16(uint32_t (&r)[16], uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads are complete; the registers are named so that nothing that uses
+// them moves above the wait.
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -230,13 +252,28 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 s, __half2 m) {
   return r;
 }
 
+// A warp's place in its CTA's work: kept in shared memory, so that it takes no
+// registers while a part of an item is under way.
+struct Walk {
+  Item it;
+  long at;
+  int s0, s1;  // steps of the item; s0 == s1: the range is over
+
+  __device__ __forceinline__ void cut(const KvpRange& r) {
+    const int2 my = it.part(at, r.u0, r.u1);
+    s0 = my.x, s1 = my.y;
+  }
+};
+
 struct Control {
   uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], last;
-  KvpRangeShared<Item> range;
+  KvpRangeShared<Item> range_sh;
+  KvpRange range;
+  Walk walk[kThreads / 32];
   // first token of each cache tile of the step, low bit: all rows see all of
   // it; -16: nothing there
-  int place[kRing][kStep];
+  alignas(16) int place[kRing][kStep];  // read four at a time
   uint32_t tmem;
   volatile int gave_up;
 };
@@ -248,6 +285,28 @@ __device__ __forceinline__ uint32_t seen16(const KvpAttendArgs& a, int p, int ba
   uint32_t m = below(p - base + 1);
   if (a.window) m &= ~below(p - a.window + 1 - base) | below(a.sinks - base);
   return m;
+}
+
+// The same for two cache tiles' places (Control::place).
+__device__ __forceinline__ uint32_t seen32(const KvpAttendArgs& a, int p, int place0, int place1) {
+  return seen16(a, p, place0 & ~1) | (seen16(a, p, place1 & ~1) << 16);
+}
+__device__ __forceinline__ void hide(uint32_t (&s)[32], uint32_t seen) {
+#pragma unroll
+  for (int i = 0; i < 32; i++) s[i] = seen >> i & 1 ? s[i] : 0xff800000u;  // -infinity
+}
+__device__ __forceinline__ float largest(const uint32_t (&s)[32]) {
+  float m[4];
+#pragma unroll
+  for (int k = 0; k < 4; k++) m[k] = __uint_as_float(s[k]);
+#pragma unroll
+  for (int i = 4; i < 32; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      m[k] = fmaxf(m[k], __uint_as_float(s[i + k]));
+      if (i + 4 < 32) m[k] = fmaxf(m[k], __uint_as_float(s[i + 4 + k]));
+    }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
 template <typename T, int D>
@@ -264,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
   pdl_trigger();
   if (tid == 0) {
     for (int t = 0; t < 2; t++) {
-      mbar_init(&ctl.q_full[t], kTileRows), mbar_init(&ctl.s_full[t], 1);
-      mbar_init(&ctl.p_full[t], kTileRows), mbar_init(&ctl.o_done[t], 1);
+      mbar_init(&ctl.q_full[t], kTileRows), mbar_init(&ctl.o_done[t], 1);
+      mbar_init(&ctl.s_full[t], 1), mbar_init(&ctl.p_full[t], kTileRows);
       mbar_init(&ctl.k_full[t], kFillWarps * 32), mbar_init(&ctl.k_empty[t], 1);
       mbar_init(&ctl.v_full[t], kFillWarps * 32), mbar_init(&ctl.v_empty[t], 1);
     }
@@ -274,10 +333,33 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
-  Item it;
-  const KvpRange range = kvp_range<kThreads, true>(a, kMinSteps, ctl.range, it);
-  if (tid == 0) pa.desc[blockIdx.x].parts = 0;
-  if (range.u0 == range.u1) return;
+  Walk& walk = ctl.walk[warp];
+  {
+    Item it;
+    const KvpRange range = kvp_range<kThreads, true>(a, kMinSteps, ctl.range_sh, it);
+    if (tid == 0) {
+      ctl.range = range;
+      if (!pa.by_item) pa.desc[blockIdx.x].parts = 0;
+    }
+    if (range.u0 == range.u1) return;
+    if (lane == 0) {
+      walk.it = it, walk.at = range.at;
+      walk.cut(range);
+    }
+  }
+  // to the next item; false at the end of the range
+  auto advance = [&]() {
+    __syncwarp();
+    const bool more = walk.it.end(walk.at) < ctl.range.u1;
+    __syncwarp();
+    if (more && lane == 0) {
+      walk.at = walk.it.end(walk.at);
+      walk.it.next(a);
+      walk.cut(ctl.range);
+    }
+    __syncwarp();
+    return more && walk.s0 < walk.s1;
+  };
   if (warp == kSoftWarps + kFillWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)),
                  "r"(512)
@@ -288,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl.tmem;  // columns: S tile 0, S tile 1 (128 each), O tile 0, O tile 1 (D each)
-  long at = range.at;
   int step_no = 0;  // steps of this CTA so far, over all segments
 
   if (warp < kSoftWarps) {
@@ -298,14 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp & 3)
     const uint32_t s_at = tmem + lanes + t * 128, o_at = tmem + lanes + 256 + t * D;
     int n_s = 0, n_o = 0;  // phases of s_full, o_done
-    for (;; at = it.end(at), it.next(a)) {
-      const int2 my = it.part(at, range.u0, range.u1);
-      const int s0 = my.x, s1 = my.y;
-      if (s0 == s1) break;
-      const int row0 = it.rt * kRows, rows = min(it.seq.n * a.group - row0, kRows);
+    if (walk.s0 < walk.s1) do {
+      const int s0 = walk.s0, s1 = walk.s1;
+      const int row0 = walk.it.rt * kRows, rows = min(walk.it.seq.n * a.group - row0, kRows);
       if (t == 0 || rows > kTileRows) {
         const int rr = row0 + min(r, rows - 1);
-        const int pos = it.seq.len - it.seq.n + kvp_by_group(a, rr);
+        const int pos = walk.it.seq.len - walk.it.seq.n + kvp_by_group(a, rr);
         // ---- the tile's queries: D / 8 lanes a row, each row scaled by a power
         // of two into fp16's range.  A negative scale turns the query around and
         // a scale of 0 becomes one that rounds away, so that the largest S is
@@ -317,8 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         for (int i = 0; i < kLanes; i++) {
           const int x = row0 + min(first_row + i * kPerWarp, rows - 1);
           w[i] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) +
-                                                      (it.seq.q0 + kvp_by_group(a, x)) * a.q_row +
-                                                      (it.g * a.group + x - kvp_by_group(a, x) * a.group) * a.q_head) + part8);
+                                                      (walk.it.seq.q0 + kvp_by_group(a, x)) * a.q_row +
+                                                      (walk.it.g * a.group + x - kvp_by_group(a, x) * a.group) * a.q_head) + part8);
         }
         int my_e = 0;
 #pragma unroll
@@ -350,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         float ref = -INFINITY, l = 0.f;
         for (int j = s0; j < s1; j++) {
           mbar_wait(&ctl.s_full[t], n_s & 1, &ctl.gave_up);
+          __syncwarp();
           n_s++;
           tc_after();
           const int ring = (step_no + j - s0) & (kRing - 1);
@@ -360,22 +440,13 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
           uint32_t s[kTokens / 32][32];
 #pragma unroll
           for (int ch = 0; ch < kTokens / 32; ch++) tc_ld32(s[ch], s_at + ch * 32);
-          tc_wait_ld();
+          tc_wait_ld(s[0]), tc_wait_ld(s[1]), tc_wait_ld(s[2]), tc_wait_ld(s[3]);
           if (!whole) {
 #pragma unroll
-            for (int ch = 0; ch < kTokens / 32; ch++) {
-              const uint32_t seen = seen16(a, pos, place[2 * ch] & ~1) | (seen16(a, pos, place[2 * ch + 1] & ~1) << 16);
-#pragma unroll
-              for (int i = 0; i < 32; i++) s[ch][i] = seen >> i & 1 ? s[ch][i] : 0xff800000u;  // -infinity
-            }
+            for (int ch = 0; ch < kTokens / 32; ch++)
+              hide(s[ch], seen32(a, pos, place[2 * ch], place[2 * ch + 1]));
           }
-          float top = -INFINITY;
-#pragma unroll
-          for (int ch = 0; ch < kTokens / 32; ch++)
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              top = fmaxf(top, fmaxf(__uint_as_float(s[ch][i]), __uint_as_float(s[ch][i + 1])));
-          top *= kappa;
+          const float top = fmaxf(fmaxf(largest(s[0]), largest(s[1])), fmaxf(largest(s[2]), largest(s[3]))) * kappa;
           if (__any_sync(0xffffffffu, top > ref + kRefGap)) {
             const float next = fmaxf(ref, top);
             const float f = next == -INFINITY ? 1.f : ex2(ref - next);
@@ -386,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
               for (int ch = 0; ch < D / 16; ch++) {
                 uint32_t o[16];
                 tc_ld16(o, o_at + ch * 16);
-                tc_wait_ld();
+                tc_wait_ld(o);
 #pragma unroll
                 for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                 tc_st16(o_at + ch * 16, o);
@@ -394,21 +465,22 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
             }
           }
           const float off = kRefShift - (ref == -INFINITY ? 0.f : ref);
-          uint64_t sums = 0;  // two fp32 sums
+          uint64_t sum0 = 0, sum1 = 0;  // two fp32 sums each
           const uint64_t kk = pair(kappa, kappa), oo = pair(off, off);
 #pragma unroll
           for (int ch = 0; ch < kTokens / 32; ch++) {
             uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = split(fma2(pair(__uint_as_float(s[ch][i]), __uint_as_float(s[ch][i + 1])), kk, oo));
-              const float p0 = ex2(y.x), p1 = ex2(y.y);
-              sums = add2(sums, pair(p0, p1));
-              p[i / 2] = pack2(p0, p1);
+            for (int i = 0; i < 32; i += 4) {
+              const float2 y0 = split(fma2(pair(__uint_as_float(s[ch][i]), __uint_as_float(s[ch][i + 1])), kk, oo));
+              const float2 y1 = split(fma2(pair(__uint_as_float(s[ch][i + 2]), __uint_as_float(s[ch][i + 3])), kk, oo));
+              const float p0 = ex2(y0.x), p1 = ex2(y0.y), p2 = ex2(y1.x), p3 = ex2(y1.y);
+              sum0 = add2(sum0, pair(p0, p1)), sum1 = add2(sum1, pair(p2, p3));
+              p[i / 2] = pack2(p0, p1), p[i / 2 + 1] = pack2(p2, p3);
             }
             tc_st16(s_at + ch * 16, p);
           }
-          const float2 sum = split(sums);
+          const float2 sum = split(add2(sum0, sum1));
           l += sum.x + sum.y;
           tc_wait_st();
           tc_before();
@@ -416,19 +488,19 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         }
 
         // ---- the row's output, or its part of it
-        mbar_wait(&ctl.o_done[t], n_o & 1, &ctl.gave_up);
-        n_o++;
+        mbar_wait(&ctl.o_done[t], n_o++ & 1, &ctl.gave_up);
+        __syncwarp();
         tc_after();
-        const bool all = s0 == 0 && s1 == it.steps;
+        const bool all = s0 == 0 && s1 == walk.it.steps;
         float* part = pa.parts + (size_t)(2 * blockIdx.x + (s0 > 0 ? 0 : 1)) * C::kPartFloats;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: zeros
         T* out = static_cast<T*>(a.out) +
-                 ((size_t)(it.seq.q0 + kvp_by_group(a, rr)) * a.h_q + it.g * a.group + rr - kvp_by_group(a, rr) * a.group) * D;
+                 ((size_t)(walk.it.seq.q0 + kvp_by_group(a, rr)) * a.h_q + walk.it.g * a.group + rr - kvp_by_group(a, rr) * a.group) * D;
 #pragma unroll
         for (int ch = 0; ch < D / 32; ch++) {
           uint32_t o[32];
           tc_ld32(o, o_at + ch * 32);
-          tc_wait_ld();
+          tc_wait_ld(o);
           if (r < rows) {
 #pragma unroll
             for (int k = 0; k < 32; k += 8) {
@@ -449,104 +521,110 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
           }
         }
         if (!all && r < rows) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(ref, l);
-        if (!all && s0 == 0 && tid == 0) {
+        if (s0 == 0 && tid == 0 && (!all || pa.by_item)) {
           KvpShared d;
-          d.q_row = it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = it.g * a.group;
-          d.parts = kvp_sharers(range, it.end(at));
+          d.q_row = walk.it.seq.q0, d.row0 = row0, d.rows = rows, d.head0 = walk.it.g * a.group;
+          d.parts = all ? 0 : kvp_sharers(ctl.range, walk.it.end(walk.at));
           d.cta = blockIdx.x;
           d.pad[0] = d.pad[1] = 0;
-          pa.desc[blockIdx.x] = d;
+          pa.desc[pa.by_item ? (walk.it.b * Item::row_tiles(a, walk.it.seq) + walk.it.rt) * a.h_kv + walk.it.g
+                             : blockIdx.x] = d;
         }
       }
       step_no += s1 - s0;
-      if (it.end(at) >= range.u1) break;
-    }
+    } while (advance());
   } else if (warp < kSoftWarps + kFillWarps) {
     regs_down<kFillRegs>();
-    // ======================= decoding: a token per thread =====================
-    const int fw = warp - kSoftWarps, tk = fw * 32 + lane, sub = tk >> 4, tt = tk & 15;
-    uint4 kc[G], vc[G], kz, vz[G / 2];
-    for (;; at = it.end(at), it.next(a)) {
-      const int2 my = it.part(at, range.u0, range.u1);
-      const int s0 = my.x, s1 = my.y;
-      if (s0 == s1) break;
-      const int32_t* pages = a.pages + (long)it.b * a.max_pages;
+    // ======================= decoding: half a token's groups per thread =======
+    constexpr int H = G / 2;
+    const int tk = tid & 127, sub = tk >> 4, tt = tk & 15, g0 = (warp - kSoftWarps) / 4 * H;
+    uint4 kc[H], vc[H], vz;  // codes; value grids (one or two groups)
+    uint2 kz;                // key grids
+    if (walk.s0 < walk.s1) do {
+      const int s0 = walk.s0, s1 = walk.s1;
+      const int32_t* pages = a.pages + (long)walk.it.b * a.max_pages;
       // the page entry of this thread's cache tile of a step (-1: none), and the tile's address
       auto entry = [&](int step) {
         const int i = step * kStep + sub;
-        if (step >= s1 || i >= it.span.tiles) return -1;
-        const int page = pages[it.span.tile(i) >> (a.page_shift - 4)];
+        if (step >= s1 || i >= walk.it.span.tiles) return -1;
+        const int page = pages[walk.it.span.tile(i) >> (a.page_shift - 4)];
         if (page >= 0 && page < a.n_pages) return page;
-        if (tt == 0) kvp_note_bad(a.bad);
+        if (tt == 0 && g0 == 0) kvp_note_bad(a.bad);
         return -1;
       };
       auto tile_of = [&](int page, int step) -> const uint8_t* {
         if (page < 0) return nullptr;
-        const int in_page = it.span.tile(step * kStep + sub) & ((1 << (a.page_shift - 4)) - 1);
-        return a.pool + ((((size_t)page * a.h_kv + it.g) << (a.page_shift - 4)) + in_page) * L::kBytes;
+        const int in_page = walk.it.span.tile(step * kStep + sub) & ((1 << (a.page_shift - 4)) - 1);
+        return a.pool + ((((size_t)page * a.h_kv + walk.it.g) << (a.page_shift - 4)) + in_page) * L::kBytes;
       };
       auto load_k = [&](const uint8_t* p) {
 #pragma unroll
-        for (int g = 0; g < G; g++)
-          kc[g] = p ? __ldcg(reinterpret_cast<const uint4*>(p + L::kKeyCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
-        kz = make_uint4(0, 0, 0, 0);
-        if (p) {
-          if constexpr (G == 4) {
-            kz = __ldcg(reinterpret_cast<const uint4*>(p + L::kKeyGrid + tt * 16));
-          } else {
-            const uint2 z = __ldcg(reinterpret_cast<const uint2*>(p + L::kKeyGrid + tt * 8));
-            kz.x = z.x, kz.y = z.y;
-          }
-        }
+        for (int g = 0; g < H; g++) kc[g] = make_uint4(0, 0, 0, 0);
+        kz = make_uint2(0, 0);
+        if (!p) return;
+#pragma unroll
+        for (int g = 0; g < H; g++)
+          kc[g] = __ldcg(reinterpret_cast<const uint4*>(p + L::kKeyCodes + ((g0 + g) * 16 + tt) * 16));
+        const uint8_t* z = p + L::kKeyGrid + (tt * G + g0) * 4;
+        if constexpr (H == 2)
+          kz = __ldcg(reinterpret_cast<const uint2*>(z));
+        else
+          kz.x = __ldcg(reinterpret_cast<const unsigned int*>(z));
       };
       auto load_v = [&](const uint8_t* p) {
 #pragma unroll
-        for (int g = 0; g < G; g++)
-          vc[g] = p ? __ldcg(reinterpret_cast<const uint4*>(p + L::kValueCodes + (g * 16 + tt) * 16)) : make_uint4(0, 0, 0, 0);
+        for (int g = 0; g < H; g++) vc[g] = make_uint4(0, 0, 0, 0);
+        vz = make_uint4(0, 0, 0, 0);
+        if (!p) return;
 #pragma unroll
-        for (int g = 0; g < G / 2; g++)
-          vz[g] = p ? __ldcg(reinterpret_cast<const uint4*>(p + L::kValueGrid + (tt >> 1) * (8 * G) + g * 16))
-                    : make_uint4(0, 0, 0, 0);
+        for (int g = 0; g < H; g++)
+          vc[g] = __ldcg(reinterpret_cast<const uint4*>(p + L::kValueCodes + ((g0 + g) * 16 + tt) * 16));
+        const uint8_t* z = p + L::kValueGrid + ((tt >> 1) * G + g0) * 8;
+        if constexpr (H == 2) {
+          vz = __ldcg(reinterpret_cast<const uint4*>(z));
+        } else {
+          const uint2 zz = __ldcg(reinterpret_cast<const uint2*>(z));
+          vz.x = zz.x, vz.y = zz.y;
+        }
       };
+      // where this thread's first 16 bytes go in a tile; the others by xor
+      const uint32_t row_at = (g0 >> 1) * 16384 + tk * 128, swz = (((g0 & 1) * 4) ^ (tk & 7)) << 4;
       auto put = [&](uint8_t* dst, int g, const uint4& codes, __half2 s, __half2 m) {
         const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
         for (int i = 0; i < 4; i++)
-          *reinterpret_cast<uint4*>(dst + (g >> 1) * 16384 + tk * 128 + ((((g & 1) * 4 + i) ^ (tk & 7)) << 4)) =
-              decode8(w[i], s, m);
+          *reinterpret_cast<uint4*>(dst + row_at + (swz ^ ((g * 4 + i) << 4))) = decode8(w[i], s, m);
       };
-      int page = entry(s0), page_next = entry(s0 + 1);
-      const uint8_t* tile = tile_of(page, s0);
+      int page_next = entry(s0 + 1);
+      const uint8_t* tile = tile_of(entry(s0), s0);
       load_k(tile);
       load_v(tile);
       for (int j = s0; j < s1; j++) {
         const int no = step_no + j - s0, st = no & 1;
         const uint32_t empty = ((no >> 1) & 1) ^ 1;
-        const int first = tile ? it.span.tile(j * kStep + sub) * 16 : -16;
-        const bool sees = tile && kvp_sees_all(a, it.span.p0, it.span.p1, first, 16);
+        const int first = tile ? walk.it.span.tile(j * kStep + sub) * 16 : -16;
+        const bool sees = tile && kvp_sees_all(a, walk.it.span.p0, walk.it.span.p1, first, 16);
         // a token that no row sees may hold anything: it counts as zeros
-        const bool live = sees || (tile && kvp_some_sees(a, it.span.p0, it.span.p1, first + tt));
+        const bool live = sees || (tile && kvp_some_sees(a, walk.it.span.p0, walk.it.span.p1, first + tt));
         const uint8_t* next = tile_of(page_next, j + 1);
         page_next = entry(j + 2);
         mbar_wait(&ctl.k_empty[st], empty, &ctl.gave_up);
-        if (tt == 0) ctl.place[no & (kRing - 1)][sub] = first | (sees ? 1 : 0);
+        if (tt == 0 && g0 == 0) ctl.place[no & (kRing - 1)][sub] = first | (sees ? 1 : 0);
         {
-          const uint32_t z[4] = {kz.x, kz.y, kz.z, kz.w};
+          const uint32_t z[2] = {live ? kz.x : 0u, live ? kz.y : 0u};
 #pragma unroll
-          for (int g = 0; g < G; g++) {
-            const __half2 sm = as_h2(live ? z[g] : 0u);
-            put(smem + C::kK + st * C::kTileBytes, g, kc[g], __low2half2(sm), __high2half2(sm));
-          }
+          for (int g = 0; g < H; g++)
+            put(smem + C::kK + st * C::kTileBytes, g, kc[g], __low2half2(as_h2(z[g])), __high2half2(as_h2(z[g])));
         }
         fence_async_smem();
         mbar_arrive(&ctl.k_full[st]);
         load_k(next);
         mbar_wait(&ctl.v_empty[st], empty, &ctl.gave_up);
         {
-          const uint32_t z[8] = {vz[0].x, vz[0].y, vz[0].z, vz[0].w, vz[G / 2 - 1].x, vz[G / 2 - 1].y, vz[G / 2 - 1].z, vz[G / 2 - 1].w};
+          const uint32_t z[4] = {live ? vz.x : 0u, live ? vz.y : 0u, live ? vz.z : 0u, live ? vz.w : 0u};
 #pragma unroll
-          for (int g = 0; g < G; g++) {
-            const __half2 ss = as_h2(live ? z[2 * g] : 0u), mm = as_h2(live ? z[2 * g + 1] : 0u);
+          for (int g = 0; g < H; g++) {
+            const __half2 ss = as_h2(z[2 * g]), mm = as_h2(z[2 * g + 1]);
             put(smem + C::kV + st * C::kTileBytes, g, vc[g], tt & 1 ? __high2half2(ss) : __low2half2(ss),
                 tt & 1 ? __high2half2(mm) : __low2half2(mm));
           }
@@ -557,52 +635,48 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
         tile = next;
       }
       step_no += s1 - s0;
-      if (it.end(at) >= range.u1) break;
-    }
+    } while (advance());
   } else {
     regs_down<kIssueRegs>();
     // ======================= the products =====================================
     if (warp == kSoftWarps + kFillWarps) {
       constexpr uint32_t kS = mma_desc(kTokens, false), kO = mma_desc(D, true);
-      int n_q[2] = {0, 0}, n_p[2] = {0, 0};  // phases of q_full, p_full
-      for (;; at = it.end(at), it.next(a)) {
-        const int2 my = it.part(at, range.u0, range.u1);
-        const int s0 = my.x, s1 = my.y;
-        if (s0 == s1) break;
-        const int tiles = it.seq.n * a.group - it.rt * kRows > kTileRows ? 2 : 1;
-        for (int j = s0; j <= s1; j++) {
-          const int no = step_no + j - s0, st = no & 1;
-          if (j < s1) mbar_wait(&ctl.k_full[st], (no >> 1) & 1, &ctl.gave_up);
-          for (int t = 0; t < tiles; t++) {
-            if (j > s0) {  // O += P V of the step before
-              const int b = no - 1, bst = b & 1;
-              if (t == 0) mbar_wait(&ctl.v_full[bst], (b >> 1) & 1, &ctl.gave_up);
+      const uint32_t q_lo = desc_lo(smem_at + C::kQ, 16), k_lo0 = desc_lo(smem_at + C::kK, 16),
+                     v_lo0 = desc_lo(smem_at + C::kV, 16384);
+      uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, no = 0;  // phases of q_full, p_full; steps so far
+      if (walk.s0 < walk.s1) do {
+        const int steps = walk.s1 - walk.s0;
+        const int tiles = walk.it.seq.n * a.group - walk.it.rt * kRows > kTileRows ? 2 : 1;
+        for (int j = 0; j <= steps; j++, no++) {
+          const uint32_t st = no & 1, bst = st ^ 1;  // stages of this step and of the one before
+          if (j < steps) mbar_wait(&ctl.k_full[st], no >> 1 & 1, &ctl.gave_up);
+          if (j > 0) mbar_wait(&ctl.v_full[bst], (no - 1) >> 1 & 1, &ctl.gave_up);
+#pragma unroll
+          for (int t = 0; t < 2; t++) {  // the tiles in turn: one's products run while the other's weights are made
+            if (t == tiles) break;
+            const uint32_t s_at = tmem + t * 128, o_at = tmem + 256 + t * D;
+            if (j > 0) {  // O += P V of the step before
               mbar_wait(&ctl.p_full[t], n_p[t]++ & 1, &ctl.gave_up);
               tc_after();
-              const uint32_t v_lo = desc_lo(smem_at + C::kV + bst * C::kTileBytes, 16384);
-              const uint32_t o_at = tmem + 256 + t * D, p_at = tmem + t * 128;
+              const uint32_t v_lo = v_lo0 + bst * (C::kTileBytes >> 4);
               if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < kTokens / 16; ks++)
-                  tc_mma_ts(o_at, p_at + ks * 8, v_lo + ks * (2048 >> 4), kDescHi, kO, ks > 0 || j - 1 > s0);
+                  tc_mma_ts(o_at, s_at + ks * 8, v_lo + ks * (2048 >> 4), kDescHi, kO, ks > 0 || j > 1);
                 if (t == tiles - 1) tc_commit(&ctl.v_empty[bst]);
-                if (j == s1) tc_commit(&ctl.o_done[t]);
+                if (j == steps) tc_commit(&ctl.o_done[t]);
               }
               __syncwarp();
             }
-            if (j < s1) {  // S = Q K
-              if (j == s0) {
-                mbar_wait(&ctl.q_full[t], n_q[t]++ & 1, &ctl.gave_up);
-                tc_after();
-              }
-              const uint32_t q_lo = desc_lo(smem_at + C::kQ + t * C::kTileBytes, 16);
-              const uint32_t k_lo = desc_lo(smem_at + C::kK + st * C::kTileBytes, 16);
-              const uint32_t s_at = tmem + t * 128;
+            if (j < steps) {  // S = Q K, over the weights that the product before has read
+              if (j == 0) mbar_wait(&ctl.q_full[t], n_q[t]++ & 1, &ctl.gave_up);
+              tc_after();
+              const uint32_t k_lo = k_lo0 + st * (C::kTileBytes >> 4), ql = q_lo + t * (C::kTileBytes >> 4);
               if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++) {
                   const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                  tc_mma_ss(s_at, q_lo + off, k_lo + off, kDescHi, kDescHi, kS, ks > 0);
+                  tc_mma_ss(s_at, ql + off, k_lo + off, kDescHi, kDescHi, kS, ks > 0);
                 }
                 tc_commit(&ctl.s_full[t]);
                 if (t == tiles - 1) tc_commit(&ctl.k_empty[st]);
@@ -611,9 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
             }
           }
         }
-        step_no += s1 - s0;
-        if (it.end(at) >= range.u1) break;
-      }
+        no--;  // the last pass made no step
+      } while (advance());
       if (elect_one()) tc_commit(&ctl.last);  // nothing is in flight when TMEM is given back
       __syncwarp();
       for (unsigned long long t0 = now_ns(); !mbar_try(&ctl.last, 0) && now_ns() - t0 < kWaitNs;) {
@@ -628,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
   }
 }
 
-// One CTA per (CTA of the pass, 4 or 8 rows): joins the parts of the item that
-// starts there, in the order of the CTAs; 4 elements per thread.
+// One CTA per (item, 4 or 8 rows): joins the parts of the item, in the order of
+// the CTAs; 4 elements per thread.
 constexpr int kMergeThreads = 128;
 
 template <typename T, int D>
@@ -643,7 +716,7 @@ __global__ void __launch_bounds__(kMergeThreads) kvp_prefill_merge_kernel(const 
   const int r = blockIdx.y * kPer + threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4) * 4;
   if (d.parts == 0 || r >= d.rows) return;
   auto part = [&](int i) {  // the first lies in the starting CTA's second place, the others in their CTA's first
-    return pa.parts + (size_t)(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * C::kPartFloats;
+    return pa.parts + (size_t)(2 * (d.cta + i) + (i == 0 ? 1 : 0)) * C::kPartFloats;
   };
   float top = -INFINITY;
   for (int i = 0; i < d.parts; i++) top = fmaxf(top, part(i)[kRows * D + 2 * r]);
@@ -660,8 +733,8 @@ __global__ void __launch_bounds__(kMergeThreads) kvp_prefill_merge_kernel(const 
     l = fmaf(f, m.y, l);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int qi = d.q_row + (d.row0 + r) / a.group, h = d.head0 + (d.row0 + r) % a.group;
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((size_t)qi * a.h_q + h) * D + d4) =
+  const int qi = kvp_by_group(a, d.row0 + r), h = d.head0 + d.row0 + r - qi * a.group;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + ((size_t)(d.q_row + qi) * a.h_q + h) * D + d4) =
       make_uint2(Elem<T>::from_float2(sum.x * inv, sum.y * inv), Elem<T>::from_float2(sum.z * inv, sum.w * inv));
 }
 
@@ -673,10 +746,15 @@ sf_status launch_prefill(const KvpAttendArgs& a, cudaStream_t s) {
   pa.a = a;
   pa.desc = static_cast<KvpShared*>(a.ws);
   pa.parts = reinterpret_cast<float*>(pa.desc + ctas);
+  const long each = (long)(a.n_q / a.batch) * a.group;
+  const long items = (each + kRows - 1) / kRows * a.h_kv * a.batch;
+  pa.by_item = !a.cu_q && items < ctas;
+  const int entries = pa.by_item ? (int)items : ctas;
+  const int most = a.cu_q ? kRows : (int)(each < kRows ? each : kRows), per = kMergeThreads / (D / 4);
   SF_CUDA((kvp_allow_smem<kvp_prefill_kernel<T, D>>(C::kSmem)));
   SF_CUDA(launch_pdl(kvp_prefill_kernel<T, D>, dim3(ctas), dim3(kThreads), C::kSmem, s, pa));
-  SF_CUDA(launch_pdl(kvp_prefill_merge_kernel<T, D>, dim3(ctas, kRows / (kMergeThreads / (D / 4))), dim3(kMergeThreads),
-                     0, s, pa));
+  SF_CUDA(launch_pdl(kvp_prefill_merge_kernel<T, D>, dim3(entries, (most + per - 1) / per), dim3(kMergeThreads), 0, s,
+                     pa));
   return SF_OK;
 }
 
