@@ -38,7 +38,10 @@ constexpr int kExtra = 8;      // an item's queries, join and output take about 
 constexpr float kRefGap = 6.f;   // log2: how far a logit may pass the reference
 constexpr float kRefShift = 9.f; // weights are 2^(x - reference + 9) <= 2^15
 
-constexpr int stages(int nt) { return nt == 4 ? 4 : 3; }
+// CTAs per SM: three while a thread's sums fit in 168 registers, two beyond (two
+// columns: 27 us against 31 with three CTAs and their spilled registers).
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+constexpr int stages(int nt) { return nt == 4 ? 4 : 3; }  // four rows' columns need the fourth for the exchange
 
 template <int D, int NT>
 struct Cfg {
@@ -119,7 +122,7 @@ __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast
 // ---- the kernel -------------------------------------------------------------
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 2 : 3) kvp_decode_kernel(const __grid_constant__ DecodeArgs da) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kvp_decode_kernel(const __grid_constant__ DecodeArgs da) {
   using L = KvpTile<D>;
   using C = Cfg<D, NT>;
   constexpr int G = L::G, MT = D / 16;
@@ -621,8 +624,15 @@ __global__ void __launch_bounds__(kMergeThreads) kvp_merge_kernel(const __grid_c
       make_uint2(Elem<T>::from_float2(sum.x * inv, sum.y * inv), Elem<T>::from_float2(sum.z * inv, sum.w * inv));
 }
 
-int row_blocks(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-int decode_ctas(int nt) { return num_sms() * (nt == 4 ? 2 : 3); }
+// Columns of 8 rows per item: as few as the rows need, in items of at most four.
+// A column costs its products and softmax, every item the decoding of the cache
+// (8 sequences of 8192 tokens, 4 KV heads, d = 128: 27 us with two columns, 32
+// with three, 40 with four).
+int row_blocks(int rows) {
+  const int blocks = (rows + 7) / 8, items = (blocks + 3) / 4;
+  return (blocks + items - 1) / items;
+}
+int decode_ctas(int nt) { return num_sms() * ctas_per_sm(nt); }
 
 template <typename T, int D, int NT>
 sf_status launch_decode(const KvpAttendArgs& a, cudaStream_t s) {
@@ -652,6 +662,7 @@ sf_status launch_decode_nt(const KvpAttendArgs& a, int rows, cudaStream_t s) {
   switch (row_blocks(rows)) {
     case 1: return launch_decode<T, D, 1>(a, s);
     case 2: return launch_decode<T, D, 2>(a, s);
+    case 3: return launch_decode<T, D, 3>(a, s);
     default: return launch_decode<T, D, 4>(a, s);
   }
 }
