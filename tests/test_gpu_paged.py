@@ -504,3 +504,105 @@ def test_python_refusals():
         with pytest.raises(abi.SFError):
             call()
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------------------
+# sizes that reach every form of the kernels (fp64 reference on the device)
+
+
+def reference(case, q, cu, b, row, window, sinks, scale):
+    """One query row of sequence b in fp64 on the device: (out, sum p|v|, largest scale sum |q||k|) per head."""
+    n = case.lens[b]
+    x = q[cu[b] + row].double()
+    p = n - (cu[b + 1] - cu[b]) + row
+    j = torch.arange(max(p + 1, 0), device="cuda")
+    if window:
+        j = j[(j > p - window) | (j < sinks)]
+    k, v = (torch.as_tensor(t[b]).cuda()[j].repeat_interleave(q.shape[1] // case.h_kv, 1) for t in (case.k, case.v))
+    w = torch.softmax(torch.einsum("hd,jhd->hj", x, k) * scale, -1)
+    lmag = abs(scale) * torch.einsum("hd,jhd->hj", x.abs(), k.abs()).amax(-1)
+    return f64(torch.einsum("hj,jhd->hd", w, v)), f64(torch.einsum("hj,jhd->hd", w, v.abs())), f64(lmag)
+
+
+def spot_check(case, out, q, cu, dtype, window, sinks, rows):
+    scale = case.d ** -0.5
+    got, qh = f64(out), f64(q)
+    for b, r in rows:
+        if case.lens[b] - (cu[b + 1] - cu[b]) + r < 0:
+            assert not got[cu[b] + r].any()
+            continue
+        ref, mag, lmag = reference(case, q, cu, b, r, window, sinks, scale)
+        tol = tolerance(dtype, ref, mag, lmag, qh[cu[b] + r], scale, np.abs(case.v[b]).max(), case.lens[b])
+        err = np.abs(got[cu[b] + r] - ref)
+        assert (err <= tol).all(), (b, r, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("batch,nq,h_kv,group,d,window", [
+    (70, 1, 8, 4, 128, 0),     # more items than CTAs
+    (30, 1, 8, 4, 64, 40),     # fewer items than CTAs: an entry each
+    (50, 3, 4, 5, 128, 0),     # two columns of rows
+    (40, 3, 2, 7, 64, 100),    # three
+    (33, 8, 2, 8, 128, 0),     # two items per sequence
+    (9, 40, 8, 4, 128, 0),     # many-row items, one tile and two
+    (40, 100, 8, 4, 64, 64),   # more of them than CTAs
+])
+def test_batches(batch, nq, h_kv, group, d, window):
+    rng = np.random.default_rng(batch)
+    lens = [int(x) for x in rng.integers(0, 700, batch)]
+    lens[3], lens[5] = 0, 1
+    case = Case(batch, lens, h_kv, d, 32)
+    q, cu = queries(case, [nq] * batch, h_kv * group, "bf16")
+    out = case.cache.attend(q, i32(case.pages), i32(lens), window=window, sinks=3)
+    again = case.cache.attend(q, i32(case.pages), i32(lens), cu_q=i32(cu), window=window, sinks=3)
+    assert torch.equal(out, again)
+    rows = [(int(b), int(r)) for b, r in zip(rng.integers(0, batch, 40), rng.integers(0, nq, 40))] + [(3, 0), (5, nq - 1)]
+    spot_check(case, out, q, cu, "bf16", window, 3, rows)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_mixed_long_batch(d):
+    """Chunks of thousands of queries, drafts and single tokens in one call; the
+    bounded waits of the kernels all end by themselves."""
+    lens, counts = [3000, 5000, 1, 2500, 700, 4096], [3000, 1000, 1, 1, 7, 4096]
+    case = Case(31, lens, 2, d, 64)
+    q, cu = queries(case, counts, 8, "fp16")
+    left, n = ctypes.c_uint(), 0
+    abi.sf_device_wait_timeouts(ctypes.byref(left), 1)
+    for window, sinks in ((0, 0), (1000, 4)):
+        for _ in range(10):
+            out = case.cache.attend(q, i32(case.pages), i32(lens), cu_q=i32(cu), window=window, sinks=sinks)
+        rows = [(b, int(r)) for b in range(6) for r in case.rng.integers(0, counts[b], 8)]
+        spot_check(case, out, q, cu, "fp16", window, sinks, rows)
+    abi.check(abi.sf_device_wait_timeouts(ctypes.byref(left), 0), "sf_device_wait_timeouts")
+
+
+def test_offsets_past_32_bits():
+    """A pool of 5 GB whose last pages are used."""
+    page, h_kv, d = 64, 8, 128
+    n_pages = 5 * 10 ** 9 // (page * h_kv * 160)
+    cache = PagedKVCache(n_pages, page, h_kv, d)
+    rng = np.random.default_rng(0)
+    k, v = rounded(tokens(rng, 200, h_kv, d), "bf16"), rounded(rng.normal(size=(200, h_kv, d)), "bf16")
+    table = np.array([[n_pages - 1, 0, n_pages - 3, n_pages // 2]])
+    slots = table[0, np.arange(200) // page] * page + np.arange(200) % page
+    cache.write(k, v, i32(slots))
+    kk, vv = cache.read(i32(slots), torch.float32)
+    assert np.array_equal(f64(kk).astype(np.float32), paged.stored(f64(k)).astype(np.float32))
+    case = Case.__new__(Case)
+    case.lens, case.h_kv, case.d, case.rng = [200], h_kv, d, rng
+    case.k, case.v = [paged.stored(f64(k))], [paged.stored(f64(v))]
+    for nq in (1, 100):
+        q, cu = queries(case, [nq], 32, "bf16")
+        out = cache.attend(q, i32(table), i32([200]))
+        spot_check(case, out, q, cu, "bf16", 0, 0, [(0, 0), (0, nq - 1)])
+
+
+def test_wide_window_is_no_window():
+    """Windows up to the largest int behave as none; sinks likewise as all."""
+    case = Case(33, [300], 1, 64, 16)
+    for nq in (1, 100):
+        q, _ = queries(case, [nq], 4, "fp16")
+        args = (q, i32(case.pages), i32([300]))
+        full = case.cache.attend(*args)
+        for window, sinks in ((300, 0), (2 ** 31 - 1, 5), (1, 2 ** 31 - 1), (7, 300)):
+            assert torch.equal(case.cache.attend(*args, window=window, sinks=sinks), full), (window, sinks)
