@@ -359,7 +359,10 @@ class PagedKVCache:
         n_q, h_q, _ = q.shape
         batch, max_pages = pages.shape
         qp, qr, qh = self._rows(q, where, "q", h_q)
-        out = self._out(out, where, "out", q.shape, q.dtype, stream)
+        if out is None and stream is None and q.is_contiguous():
+            out = torch.empty_like(q)
+        else:
+            out = self._out(out, where, "out", q.shape, q.dtype, stream)
         if ws is None:
             ws = self._out(None, where, "ws", (max(self.attend_workspace(n_q, batch, h_q), 16),), torch.uint8, stream)
         elif ws.device != self.device or not ws.is_contiguous():
