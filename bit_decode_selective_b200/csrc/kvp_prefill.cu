@@ -24,6 +24,15 @@
 // masked code word gives them up: queries and keys alike, and the output's
 // columns are put back in order when they are stored.
 //
+// What bounds it: each tile's chain of softmax (2,750 cycles for 128 tokens: 128
+// exponentials a thread at 8 cycles and warp on the special-function unit, shared
+// by two warps, are 1,700 of them) and products (1,800 for 16 that take 1,034 back
+// to back).  Two tiles in turn keep the tensor cores 45% busy; TMEM has no room for
+// a third.  2,048 bf16 queries of 32 heads (8 KV heads, d = 128) behind 16,384
+// tokens: 0.49 ms = 1.05 PFLOP/s; 8,192 behind 8,192: 0.58 ms = 0.95; 4,096 with a
+// window of 1,024: 0.12 ms = 0.49 (an item's queries, first step and output cost
+// 9 us and are not hidden).
+//
 // The work is cut into equal ranges on the device (kvp_attend.cuh); every wait
 // is bounded.
 #include "internal.cuh"
@@ -43,8 +52,10 @@ constexpr int kSoftRegs = 160, kFillRegs = 56, kIssueRegs = 48;
 constexpr int kRing = 4;                 // steps whose token places are kept
 constexpr float kRefGap = 6.f, kRefShift = 9.f;
 constexpr unsigned long long kWaitNs = 1000000000ull;  // bounded waits give up after 1 s
-constexpr int kMinSteps = 1;
-constexpr int kExtra = 4;                // an item's queries and output take about as long as 4 steps
+constexpr int kMinSteps = 1;             // the fewest steps worth a CTA
+// An item's queries and output take about as long as 4 steps (two prompts of 2,000
+// and 4,001 tokens, window 1,024: 191 us with 4, 207 with 2, 193 with 9).
+constexpr int kExtra = 4;
 
 __device__ unsigned int g_wait_timeouts;
 

@@ -263,17 +263,18 @@ class PagedKVCache:
         self.desc = abi.sf_kvp(n_pages, page, h_kv, d, pool.data_ptr())
         self._ref = ctypes.byref(self.desc)
         self._ws_bytes = {}
+        self._index_of_device = self.device.index
+        self._fn = {name: getattr(abi.lib(), name) for name in ("sf_kvp_write", "sf_kvp_read", "sf_kvp_attend")}
 
     def _run(self, where, stream, *args):
         """The entry point on `stream` (default: the current one) of the cache's device."""
-        fn = getattr(abi.lib(), where)
-        index = self.device.index
+        index = self._index_of_device
         s = _current_stream(index) if stream is None else stream.cuda_stream
         if torch.cuda.current_device() == index:
-            status = fn(self._ref, *args, s)
+            status = self._fn[where](self._ref, *args, s)
         else:
             with torch.cuda.device(index):
-                status = fn(self._ref, *args, s)
+                status = self._fn[where](self._ref, *args, s)
         if status:
             check(status, where)
 
@@ -321,7 +322,8 @@ class PagedKVCache:
             raise _refuse(where, "dtype must be fp16, bf16 or fp32")
         n = slots.numel()
         shape = (n, self.h_kv, self.d)
-        k, v = (self._out(t, where, name, shape, dtype, stream) for t, name in ((k, "k"), (v, "v")))
+        k = self._out(k, where, "k", shape, dtype, stream)
+        v = torch.empty_like(k) if v is None and stream is None else self._out(v, where, "v", shape, dtype, stream)
         self._run(where, stream, self._index(slots, where, "slots", n), n, k.data_ptr(), v.data_ptr(), _DTYPES[dtype],
                   self._bad(bad, where))
         return k, v
@@ -338,10 +340,12 @@ class PagedKVCache:
 
     def attend_workspace(self, n_q: int, batch: int, h_q: int) -> int:
         key = (n_q, batch, h_q)
-        if key not in self._ws_bytes:
+        need = self._ws_bytes.get(key)
+        if need is None:
             with torch.cuda.device(self.device):
-                self._ws_bytes[key] = abi.sf_kvp_attend_workspace_bytes(self._ref, n_q, batch, h_q)
-        return self._ws_bytes[key]
+                need = abi.sf_kvp_attend_workspace_bytes(self._ref, n_q, batch, h_q)
+            self._ws_bytes[key] = need
+        return need
 
     def attend(self, q, pages, lens, cu_q=None, scale=None, window: int = 0, sinks: int = 0, out=None, bad=None,
                ws=None, stream=None):
@@ -364,7 +368,9 @@ class PagedKVCache:
         else:
             out = self._out(out, where, "out", q.shape, q.dtype, stream)
         if ws is None:
-            ws = self._out(None, where, "ws", (max(self.attend_workspace(n_q, batch, h_q), 16),), torch.uint8, stream)
+            ws = self.pool.new_empty(self.attend_workspace(n_q, batch, h_q))
+            if stream is not None:
+                ws.record_stream(stream)
         elif ws.device != self.device or not ws.is_contiguous():
             raise _refuse(where, "ws must be contiguous, on the cache's device")
         self._run(where, stream, qp, qr, qh, _DTYPES[q.dtype], n_q,

@@ -221,10 +221,9 @@ SF_API sf_status sf_gemv_refined_split(const sf_wq* w, const uint16_t* x, int ba
                                 float* y_corr, sf_stream_t stream);
 
 /* Number of bounded device-side waits that ran out on the current device
- * (*count), optionally reset to 0 (reset != 0).  The refined GEMV and the paged
- * cache's attention wait on
- * shared-memory barriers for its bulk copies; each such wait gives up after one
- * second, counts itself here and lets the kernel finish without its result
+ * (*count), optionally reset to 0 (reset != 0).  The refined GEMV waits on
+ * shared-memory barriers for its bulk copies, the paged cache's attention for
+ * its products; each such wait gives up after one second, counts itself here and lets the kernel finish without its result
  * (the output is then undefined), so a fault in the memory system shows up as
  * a count, not as a hung GPU.  A nonzero count makes this call return
  * SF_ERR_TIMEOUT.  The call synchronises with the device (it reads the counter
@@ -388,8 +387,8 @@ SF_API sf_status sf_kv_attend_selective_static(const sf_kv* kv, int t, const uin
 /* Element types of the paged cache's inputs and outputs. */
 typedef enum { SF_F16 = 0, SF_BF16 = 1, SF_F32 = 2 } sf_dtype;
 
-/* A pool of `n_pages` pages of `page` tokens, shared by any number of
- * sequences ([ABS]: low-bit KV caches; the pages leave the placement open).
+/* A pool of `n_pages` cache pages of `page` tokens, shared by any number of
+ * sequences ([ABS]: low-bit KV caches; their placement is left open there).
  * Each token and KV head is quantised to plain 4-bit codes (the quantisation
  * at the top of this file with b = 4, r = 0) in groups of 32 consecutive
  * elements, with two departures: a NaN counts as 0, and values are first
@@ -451,13 +450,18 @@ SF_API sf_status sf_kvp_read(const sf_kvp* kv, const int32_t* slots, int n, void
  *     sequence; only entries that hold visible tokens are read;
  *   lens [batch] int32 DEVICE: cached tokens per sequence, the queries' own
  *     included.
- *   h_q % h_kv == 0; scale finite; window, sinks >= 0.
+ *   h_q % h_kv == 0; scale finite; window, sinks >= 0; batch <= 65535;
+ *   n_q * h_q < 2^30; out does not overlap q.
  * Device-side arguments are checked there: a length is clamped to [0,
  * max_pages * page], cu_q to [0, n_q], and the tokens of a page index outside
  * [0, n_pages) are not read and not seen; each makes *bad (nullable, a device
  * int32) nonzero.
- * q must be finite in every row that is to be finite: a row with a NaN or an
- * infinity spoils its own output only.
+ * q must be finite, and below 2^100 in magnitude, in every row that is to be
+ * finite: a row with a NaN or an infinity spoils its own output only.
+ * Precision: logits are fp32 sums (of exact products for sequences with at most
+ * 64 rows, queries x query heads per KV head; beyond that keys are rounded once
+ * to fp16); values and softmax weights are rounded once to fp16, the weights
+ * relative to their largest; the sums over tokens are fp32.
  * ws: sf_kvp_attend_workspace_bytes() bytes, 16-byte aligned, contents
  * irrelevant before and after; calls that overlap on the GPU need one each. */
 SF_API sf_status sf_kvp_attend(const sf_kvp* kv, const void* q, int64_t q_row, int64_t q_head, sf_dtype dtype,
