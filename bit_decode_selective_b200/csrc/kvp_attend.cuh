@@ -195,8 +195,8 @@ __device__ __forceinline__ long kvp_scan(long x) {  // inclusive sum over the la
 }
 
 // kvp_range for batches of at most 32 * kKvpFew sequences with few row tiles:
-// every warp finds the place by itself, without a barrier (one sequence of 8192
-// tokens: 11.4 us against 11.7).
+// every warp finds the place by itself, without a barrier (0.3 us of a call with
+// one sequence of 8192 tokens).
 constexpr int kKvpFew = 2;
 template <typename Item>
 __device__ __forceinline__ KvpRange kvp_range_few(const KvpAttendArgs& a, int min_steps, Item& it) {

@@ -555,7 +555,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) kvp_decode_kernel(c
 // mod 2048 / D, the shares are summed and then added in order, whatever the form:
 // a CTA takes ROWS rows of an item, 512 / ROWS threads a row, 4 elements and
 // ROWS shares a thread.  With few items each row has a CTA of its own, so that
-// its parts' loads are all under way at once.
+// its parts' loads are all under way at once.  A CTA whose rows all lie behind the
+// item's leaves at once: so the row of a one-row CTA is known to exist (one query
+// at 8192 tokens, the whole call: 11.4 -> 10.5 us).
 constexpr int kMergeThreads = 512;
 
 template <typename T, int D, int NT, int ROWS>
@@ -569,7 +571,7 @@ __global__ void __launch_bounds__(kMergeThreads) kvp_merge_kernel(const __grid_c
   pdl_wait();
   const KvpShared d = da.desc[blockIdx.x];
   const int rt = threadIdx.x / kPer, r = blockIdx.y * ROWS + rt, tid = threadIdx.x % kPer;
-  if (d.parts == 0) return;
+  if (d.parts == 0 || blockIdx.y * ROWS >= d.rows) return;
   const bool live = r < d.rows;
   const int q4 = tid % (D / 4);
 #pragma unroll 1

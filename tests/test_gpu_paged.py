@@ -559,6 +559,18 @@ def test_batches(batch, nq, h_kv, group, d, window):
     spot_check(case, out, q, cu, "bf16", window, 3, rows)
 
 
+@pytest.mark.parametrize("h_kv,group,d", [(1, 64, 128), (1, 65, 64), (2, 80, 128), (1, 300, 64)])
+def test_many_heads_per_kv_head(h_kv, group, d):
+    """One query per sequence whose heads alone fill the few-row kernel or go
+    to the many-row one, up to more than one of its tiles."""
+    lens = [300, 0, 1, 2049]
+    case = Case(group, lens, h_kv, d, 16)
+    q, cu = queries(case, [1] * 4, h_kv * group, "bf16")
+    out = case.cache.attend(q, i32(case.pages), i32(lens), window=200, sinks=2)
+    check(case, out, q, cu, "bf16", 200, 2, d ** -0.5)
+    assert torch.equal(out, case.cache.attend(q, i32(case.pages), i32(lens), cu_q=i32(cu), window=200, sinks=2))
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_mixed_long_batch(d):
     """Chunks of thousands of queries, drafts and single tokens in one call; the
