@@ -344,6 +344,8 @@ class PagedKVCache:
         if need is None:
             with torch.cuda.device(self.device):
                 need = abi.sf_kvp_attend_workspace_bytes(self._ref, n_q, batch, h_q)
+            if len(self._ws_bytes) >= 1024:  # ragged batches come in endless shapes
+                self._ws_bytes.clear()
             self._ws_bytes[key] = need
         return need
 

@@ -559,6 +559,14 @@ def test_batches(batch, nq, h_kv, group, d, window):
     spot_check(case, out, q, cu, "bf16", window, 3, rows)
 
 
+def test_workspace_sizes_kept():
+    """A server's batches come in ever new shapes: what is kept of them is bounded."""
+    cache = PagedKVCache(1, 16, 1, 64)
+    sizes = [cache.attend_workspace(n, 1, 4) for n in range(1, 2500)]
+    assert len(cache._ws_bytes) <= 1024
+    assert sizes == [cache.attend_workspace(n, 1, 4) for n in range(1, 2500)]
+
+
 @pytest.mark.parametrize("h_kv,group,d", [(1, 64, 128), (1, 65, 64), (2, 80, 128), (1, 300, 64)])
 def test_many_heads_per_kv_head(h_kv, group, d):
     """One query per sequence whose heads alone fill the few-row kernel or go
