@@ -20,6 +20,21 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(like, shape, dtype, stream, returned=True):
+    """A new tensor on `like`'s device that work on `stream` (None: the current one)
+    writes first.  It belongs to that stream: memory that the current stream has
+    given back may still be in use by work queued there, which `stream` does not
+    wait for.  `returned`: the caller gets it, so once dropped it is not used again
+    before the work that the current stream holds by then."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def _f16(t: torch.Tensor) -> torch.Tensor:
     assert t.dtype in (torch.float16, torch.int16, torch.uint16), t.dtype
     assert t.is_cuda and t.is_contiguous()
@@ -249,7 +264,11 @@ class PagedKVCache:
     4-bit codes with fp16 grids over 32 elements (format: include/sf.h, sf_kvp).
     Sequences of any length share it through page tables; the slot of a token is
     page_index * page + place in the page.  `pool`: an existing buffer of that
-    format instead of a new one."""
+    format instead of a new one.
+
+    Calls with `stream` run there, and the caller orders that stream behind the
+    work that fills their arguments and before the work that uses their results.
+    Memory that a call allocates itself needs no such order."""
 
     def __init__(self, n_pages: int, page: int, h_kv: int, d: int = 128, device="cuda", pool=None):
         size = ctypes.c_size_t()
@@ -331,10 +350,8 @@ class PagedKVCache:
     def _out(self, t, where, name, shape, dtype, stream):
         """An output of the given shape: `t` where it is given, else a new tensor."""
         if t is None:
-            t = self.pool.new_empty(shape, dtype=dtype)
-            if stream is not None:
-                t.record_stream(stream)
-        elif t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            return _empty(self.pool, shape, dtype, stream)
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:
             raise _refuse(where, f"{name} must be contiguous {dtype} of shape {tuple(shape)} on {self.device}")
         return t
 
@@ -370,9 +387,7 @@ class PagedKVCache:
         else:
             out = self._out(out, where, "out", q.shape, q.dtype, stream)
         if ws is None:
-            ws = self.pool.new_empty(self.attend_workspace(n_q, batch, h_q))
-            if stream is not None:
-                ws.record_stream(stream)
+            ws = _empty(self.pool, self.attend_workspace(n_q, batch, h_q), torch.uint8, stream, returned=False)
         elif ws.device != self.device or not ws.is_contiguous():
             raise _refuse(where, "ws must be contiguous, on the cache's device")
         self._run(where, stream, qp, qr, qh, _DTYPES[q.dtype], n_q,

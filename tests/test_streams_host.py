@@ -1,0 +1,83 @@
+"""Which stream the memory of a call belongs to, on the host: the launches, the
+allocator and the streams are stand-ins that note who asked for what."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+from bit_decode_selective_b200 import ops
+
+CPU = torch.device("cpu")
+I32 = dict(dtype=torch.int32)
+
+
+class Memory:
+    """An allocation: the stream it belongs to and the streams it waits for before it is used again."""
+
+    def __init__(self, shape, dtype, owner):
+        self.shape, self.dtype, self.owner, self.device = torch.Size(shape) if not isinstance(shape, int) else (shape,), dtype, owner, CPU
+        self.recorded = []
+
+    def data_ptr(self):
+        return id(self)
+
+    nbytes = 1 << 30
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+class Streams:
+    """The current stream and everything that was allocated, in order."""
+
+    def __init__(self, monkeypatch):
+        self.main, self.side = (types.SimpleNamespace(cuda_stream=h, device=CPU) for h in (0, 7))
+        self.now, self.memory, self.launches = self.main, [], []
+        monkeypatch.setattr(torch.cuda, "stream", self.on)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.now)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        monkeypatch.setattr(ops, "_current_stream", lambda index: self.now.cuda_stream)
+
+    @contextlib.contextmanager
+    def on(self, stream):
+        before, self.now = self.now, stream if stream is not None else self.now
+        yield
+        self.now = before
+
+    def new_empty(self, shape, dtype=torch.uint8):
+        self.memory.append(Memory(shape, dtype, self.now))
+        return self.memory[-1]
+
+    def launch(self, *args):
+        self.launches.append(args[-1])
+        return 0
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    return Streams(monkeypatch)
+
+
+def paged_cache(streams):
+    cache = ops.PagedKVCache.__new__(ops.PagedKVCache)
+    cache.n_pages, cache.page, cache.h_kv, cache.d = 4, 16, 2, 64
+    cache.device, cache._index_of_device, cache._ref = CPU, 0, None
+    cache.pool = types.SimpleNamespace(new_empty=streams.new_empty, device=CPU)
+    cache._ws_bytes = {(3, 1, 2): 4096}
+    cache._fn = {name: streams.launch for name in ("sf_kvp_write", "sf_kvp_read", "sf_kvp_attend")}
+    return cache
+
+
+def test_paged_calls_allocate_on_the_stream_that_writes(streams):
+    cache = paged_cache(streams)
+    q = torch.zeros(3, 2, 64, dtype=torch.float16)
+    pages, lens, slots = torch.zeros(1, 1, **I32), torch.zeros(1, **I32), torch.zeros(3, **I32)
+    cache.attend(q, pages, lens, stream=streams.side)
+    out, ws = streams.memory
+    assert out.owner is streams.side and ws.owner is streams.side
+    assert out.recorded == [streams.main]  # the caller's stream may still use it when it is dropped
+    cache.read(slots, stream=streams.side)
+    for t in streams.memory[2:]:
+        assert t.owner is streams.side and t.recorded == [streams.main]
+    assert len(streams.memory) == 4 and streams.launches == [7, 7] and streams.now is streams.main
