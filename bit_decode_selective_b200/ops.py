@@ -35,6 +35,15 @@ def _empty(like, shape, dtype, stream, returned=True):
     return t
 
 
+def _used_on(stream, *tensors):
+    """The memory of `tensors` (None: not given) is not used again before the work
+    that `stream` holds when they are dropped."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _f16(t: torch.Tensor) -> torch.Tensor:
     assert t.dtype in (torch.float16, torch.int16, torch.uint16), t.dtype
     assert t.is_cuda and t.is_contiguous()
@@ -268,7 +277,8 @@ class PagedKVCache:
 
     Calls with `stream` run there, and the caller orders that stream behind the
     work that fills their arguments and before the work that uses their results.
-    Memory that a call allocates itself needs no such order."""
+    Memory that a call allocates itself needs no such order, and tensors given to
+    one may be dropped as soon as it returns."""
 
     def __init__(self, n_pages: int, page: int, h_kv: int, d: int = 128, device="cuda", pool=None):
         size = ctypes.c_size_t()
@@ -332,6 +342,7 @@ class PagedKVCache:
         vp, vr, vh = self._rows(v, where, "v", self.h_kv) if v is not None else (None, 0, 0)
         self._run(where, stream, kp, kr, kh, vp, vr, vh, _DTYPES[some.dtype], n,
                   self._index(slots, where, "slots", n), self._bad(bad, where))
+        _used_on(stream, k, v, slots, bad, self.pool)
 
     def read(self, slots, dtype=torch.float16, k=None, v=None, bad=None, stream=None):
         """The values of `slots` [n] int32: (k, v), each [n][h_kv][d] of `dtype`
@@ -345,6 +356,7 @@ class PagedKVCache:
         v = torch.empty_like(k) if v is None and stream is None else self._out(v, where, "v", shape, dtype, stream)
         self._run(where, stream, self._index(slots, where, "slots", n), n, k.data_ptr(), v.data_ptr(), _DTYPES[dtype],
                   self._bad(bad, where))
+        _used_on(stream, slots, k, v, bad, self.pool)
         return k, v
 
     def _out(self, t, where, name, shape, dtype, stream):
@@ -395,4 +407,5 @@ class PagedKVCache:
                   self._index(pages, where, "pages", batch, max_pages), max_pages,
                   self._index(lens, where, "lens", batch), batch, h_q, self.d ** -0.5 if scale is None else scale,
                   window, sinks, out.data_ptr(), self._bad(bad, where), ws.data_ptr(), ws.nbytes)
+        _used_on(stream, q, pages, lens, cu_q, out, bad, ws, self.pool)
         return out

@@ -53,3 +53,48 @@ def test_memory_given_back_on_the_current_stream_is_not_taken():
         assert not given_back & {t.data_ptr() for t in call()}
         del held
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_arguments_may_be_dropped(nq):
+    """Temporaries given to a call on another stream are not overwritten before it has read them."""
+    case = Case(45, [3000, 2500], 2, 128, 64)
+    q, _ = queries(case, [nq, nq], 8, "fp16")
+    pages, lens = i32(case.pages), i32(case.lens)
+    want = case.cache.attend(q, pages, lens)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        outs = []
+        for _ in range(10):
+            temp, p, n = q.clone(), pages.clone(), lens.clone()
+            side.wait_stream(torch.cuda.current_stream())
+            outs.append(case.cache.attend(temp, p, n, stream=side))
+            del temp, p, n
+            for like in (q, pages, lens):
+                torch.full_like(like, 7)  # takes what was given back
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for out in outs)
+
+
+def test_side_stream_inside_a_capture():
+    """A call on a stream that a capture has forked to, its memory from the capture's own."""
+    case = Case(47, [300], 2, 64, 16)
+    q, _ = queries(case, [1], 8, "bf16")
+    args = (i32(case.pages), i32(case.lens))
+    want = case.cache.attend(q, *args)
+    side = torch.cuda.Stream()
+    qq, out = torch.zeros_like(q), torch.empty_like(q)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        a = case.cache.attend(qq + 0, *args, stream=side)
+        b = case.cache.attend(qq, *args)
+        torch.cuda.current_stream().wait_stream(side)
+        out.copy_(a)
+    for x in (q, -q, q):
+        qq.copy_(x)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, case.cache.attend(x, *args)) and torch.equal(b, out)
+    assert torch.equal(out, want)

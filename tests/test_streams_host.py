@@ -1,7 +1,6 @@
 """Which stream the memory of a call belongs to, on the host: the launches, the
 allocator and the streams are stand-ins that note who asked for what."""
 import contextlib
-import types
 
 import pytest
 import torch
@@ -28,12 +27,18 @@ class Memory:
         self.recorded.append(stream)
 
 
+class FakeStream:
+    def __init__(self, handle):
+        self.cuda_stream, self.device = handle, CPU
+
+
 class Streams:
     """The current stream and everything that was allocated, in order."""
 
     def __init__(self, monkeypatch):
-        self.main, self.side = (types.SimpleNamespace(cuda_stream=h, device=CPU) for h in (0, 7))
-        self.now, self.memory, self.launches = self.main, [], []
+        self.main, self.side = (FakeStream(h) for h in (0, 7))
+        self.now, self.memory, self.launches, self.recorded = self.main, [], [], []
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, stream: self.recorded.append((id(t), stream)))
         monkeypatch.setattr(torch.cuda, "stream", self.on)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: self.now)
         monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
@@ -63,7 +68,8 @@ def paged_cache(streams):
     cache = ops.PagedKVCache.__new__(ops.PagedKVCache)
     cache.n_pages, cache.page, cache.h_kv, cache.d = 4, 16, 2, 64
     cache.device, cache._index_of_device, cache._ref = CPU, 0, None
-    cache.pool = types.SimpleNamespace(new_empty=streams.new_empty, device=CPU)
+    cache.pool = Memory((1,), torch.uint8, streams.main)
+    cache.pool.new_empty = streams.new_empty
     cache._ws_bytes = {(3, 1, 2): 4096}
     cache._fn = {name: streams.launch for name in ("sf_kvp_write", "sf_kvp_read", "sf_kvp_attend")}
     return cache
@@ -76,8 +82,30 @@ def test_paged_calls_allocate_on_the_stream_that_writes(streams):
     cache.attend(q, pages, lens, stream=streams.side)
     out, ws = streams.memory
     assert out.owner is streams.side and ws.owner is streams.side
-    assert out.recorded == [streams.main]  # the caller's stream may still use it when it is dropped
+    assert streams.main in out.recorded  # the caller's stream may still use it when it is dropped
     cache.read(slots, stream=streams.side)
     for t in streams.memory[2:]:
-        assert t.owner is streams.side and t.recorded == [streams.main]
+        assert t.owner is streams.side and streams.main in t.recorded
     assert len(streams.memory) == 4 and streams.launches == [7, 7] and streams.now is streams.main
+
+
+def test_paged_calls_keep_what_they_are_given(streams):
+    """Tensors given to a call on another stream are kept until its work is done; on
+    the current stream nothing needs keeping."""
+    cache = paged_cache(streams)
+    k, v, q = (torch.zeros(3, 2, 64, dtype=torch.float16) for _ in range(3))
+    pages, lens, cu, bad, slots = (torch.zeros(s, **I32) for s in ((1, 1), 1, 2, 1, 3))
+    out, ws, kk, vv = torch.zeros_like(q), torch.zeros(4096, dtype=torch.uint8), torch.zeros_like(k), torch.zeros_like(v)
+    calls = {
+        lambda s: cache.write(k, v, slots, bad=bad, stream=s): (k, v, slots, bad),
+        lambda s: cache.read(slots, k=kk, v=vv, bad=bad, stream=s): (slots, kk, vv, bad),
+        lambda s: cache.attend(q, pages, lens, cu_q=cu, out=out, bad=bad, ws=ws, stream=s): (q, pages, lens, cu, out, bad, ws),
+    }
+    for call, given in calls.items():
+        streams.recorded.clear(), cache.pool.recorded.clear()
+        call(None)
+        assert not streams.recorded and not cache.pool.recorded
+        call(streams.side)
+        assert {(id(t), streams.side) for t in given} <= set(streams.recorded)
+        assert cache.pool.recorded == [streams.side]
+    assert not streams.memory
