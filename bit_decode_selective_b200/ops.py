@@ -80,8 +80,8 @@ class QuantWeights:
         x_cal = _f16(x_cal)
         n_cal = x_cal.shape[0]
         nbytes = abi.sf_fit_refinements_workspace_bytes(self.n, self.k, n_cal, chunk, kch)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
-        delta = torch.empty((self.n, self.k), dtype=torch.float64, device=w.device) if want_delta else None
+        ws = _empty(w, nbytes, torch.uint8, stream, returned=False)
+        delta = _empty(w, (self.n, self.k), torch.float64, stream) if want_delta else None
         check(abi.sf_fit_refinements(_p(w), ctypes.byref(self.desc), _p(x_cal), n_cal, chunk, kch, alpha, _p(delta),
                                      _p(ws), nbytes, _stream(stream)), "sf_fit_refinements")
         return delta
@@ -102,12 +102,12 @@ class QuantWeights:
         x = _f16(x if x.dim() == 2 else x.view(1, -1))
         batch = x.shape[0]
         if y is None:
-            y = torch.empty((batch, self.n), dtype=torch.float32, device=x.device)
+            y = _empty(x, (batch, self.n), torch.float32, stream)
         if kch > 0 and sel_in is None and sel_out is None:
-            sel_out = torch.empty((batch, self.k // chunk, kch), dtype=torch.int32, device=x.device)
+            sel_out = _empty(x, (batch, self.k // chunk, kch), torch.int32, stream)
         if ws is None:
             need = abi.sf_gemv_workspace_bytes(ctypes.byref(self.desc), batch, chunk, kch)
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+            ws = _empty(x, max(need, 16), torch.uint8, stream, returned=False)
         check(abi.sf_gemv_refined(ctypes.byref(self.desc), _p(x), batch, chunk, kch, _p(sel_in),
                                   _p(sel_out), _p(refine_rows), _p(y), _p(ws), ws.numel(), _stream(stream)),
               "sf_gemv_refined")
@@ -130,9 +130,9 @@ class QuantWeights:
         x = _f16(x if x.dim() == 2 else x.view(1, -1))
         batch = x.shape[0]
         if y_base is None:
-            y_base = torch.empty((batch, self.n), dtype=torch.float32, device=x.device)
+            y_base = _empty(x, (batch, self.n), torch.float32, stream)
         if y_corr is None:
-            y_corr = torch.empty((batch, self.n), dtype=torch.float32, device=x.device)
+            y_corr = _empty(x, (batch, self.n), torch.float32, stream)
         check(abi.sf_gemv_refined_split(ctypes.byref(self.desc), _p(x), batch, chunk, kch, _p(sel),
                                         _p(refine_rows), _p(y_base), _p(y_corr), _stream(stream)),
               "sf_gemv_refined_split")
@@ -143,7 +143,7 @@ def select_channels(x: torch.Tensor, chunk: int = 1024, kch: int = 32, sel=None,
     x = _f16(x if x.dim() == 2 else x.view(1, -1))
     batch, k = x.shape
     if sel is None:
-        sel = torch.empty((batch, k // chunk, kch), dtype=torch.int32, device=x.device)
+        sel = _empty(x, (batch, k // chunk, kch), torch.int32, stream)
     check(abi.sf_select_channels(_p(x), batch, k, chunk, kch, _p(sel), _stream(stream)),
           "sf_select_channels")
     return sel
@@ -188,16 +188,15 @@ class KVCache:
                      stream=None):
         q = _f16(q)
         h_q = q.shape[1]
-        dev = q.device
         if logits is None and want_logits:
-            logits = torch.empty((self.batch, h_q, t), dtype=torch.float32, device=dev)
+            logits = _empty(q, (self.batch, h_q, t), torch.float32, stream)
         if scores is None and want_scores:
-            scores = torch.empty((self.batch, self.h_kv, t), dtype=torch.float32, device=dev)
+            scores = _empty(q, (self.batch, self.h_kv, t), torch.float32, stream)
         if sel is None:
-            sel = torch.empty((self.batch, self.h_kv, k_tok), dtype=torch.int32, device=dev)
+            sel = _empty(q, (self.batch, self.h_kv, k_tok), torch.int32, stream)
         need = self.score_select_workspace(t, h_q, k_tok, logits is not None)
         if ws is None:
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            ws = _empty(q, max(need, 16), torch.uint8, stream, returned=False)
         check(abi.sf_kv_score_select(ctypes.byref(self.desc), t, _p(q), h_q, k_tok, _p(sel), _p(logits),
                                      _p(scores), _p(ws), ws.numel(), _stream(stream)),
               "sf_kv_score_select")
@@ -208,10 +207,10 @@ class KVCache:
         q = _f16(q)
         h_q = q.shape[1]
         if logits is None:
-            logits = torch.empty((self.batch, h_q, t), dtype=torch.float32, device=q.device)
+            logits = _empty(q, (self.batch, h_q, t), torch.float32, stream)
         need = abi.sf_kv_logits_fma_workspace_bytes(ctypes.byref(self.desc), t, h_q)
         if ws is None:
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+            ws = _empty(q, max(need, 16), torch.uint8, stream, returned=False)
         check(abi.sf_kv_logits_fma(ctypes.byref(self.desc), t, _p(q), h_q, _p(logits), _p(ws), ws.numel(),
                                    _stream(stream)), "sf_kv_logits_fma")
         return logits
@@ -224,10 +223,10 @@ class KVCache:
         q = _f16(q)
         h_q = q.shape[1]
         if out is None:
-            out = torch.empty((self.batch, h_q, self.d), dtype=torch.float32, device=q.device)
+            out = _empty(q, (self.batch, h_q, self.d), torch.float32, stream)
         need = self.attn_workspace(t, h_q, k_tok, n_splits)
         if ws is None:
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+            ws = _empty(q, max(need, 16), torch.uint8, stream, returned=False)
         check(abi.sf_kv_attn_refined(ctypes.byref(self.desc), t, _p(q), h_q, _p(sel), k_tok, n_splits,
                                      _p(out), _p(ws), ws.numel(), _stream(stream)),
               "sf_kv_attn_refined")
@@ -242,14 +241,13 @@ class KVCache:
         """Score, select and attend in one call.  Returns (out, sel)."""
         q = _f16(q)
         h_q = q.shape[1]
-        dev = q.device
         if out is None:
-            out = torch.empty((self.batch, h_q, self.d), dtype=torch.float32, device=dev)
+            out = _empty(q, (self.batch, h_q, self.d), torch.float32, stream)
         if sel is None:
-            sel = torch.empty((self.batch, self.h_kv, k_tok), dtype=torch.int32, device=dev)
+            sel = _empty(q, (self.batch, self.h_kv, k_tok), torch.int32, stream)
         need = self.attend_workspace(t, h_q, k_tok, logits is not None)
         if ws is None:
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+            ws = _empty(q, max(need, 16), torch.uint8, stream, returned=False)
         check(abi.sf_kv_attend_selective(ctypes.byref(self.desc), t, _p(q), h_q, k_tok, _p(sel),
                                          _p(logits), _p(out), _p(ws), ws.numel(), _stream(stream)),
               "sf_kv_attend_selective")

@@ -5,7 +5,7 @@ import contextlib
 import pytest
 import torch
 
-from bit_decode_selective_b200 import ops
+from bit_decode_selective_b200 import abi, ops
 
 CPU = torch.device("cpu")
 I32 = dict(dtype=torch.int32)
@@ -20,6 +20,9 @@ class Memory:
 
     def data_ptr(self):
         return id(self)
+
+    def numel(self):
+        return self.nbytes
 
     nbytes = 1 << 30
 
@@ -109,3 +112,57 @@ def test_paged_calls_keep_what_they_are_given(streams):
         assert {(id(t), streams.side) for t in given} <= set(streams.recorded)
         assert cache.pool.recorded == [streams.side]
     assert not streams.memory
+
+
+class Half(Memory):
+    """An fp16 input on the current stream."""
+
+    is_cuda = True
+
+    def __init__(self, streams, *shape, dtype=torch.float16):
+        super().__init__(shape, dtype, streams.main)
+        self.new_empty = streams.new_empty
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+
+def weights():
+    w = ops.QuantWeights.__new__(ops.QuantWeights)
+    w.n, w.k, w.b, w.r, w.group, w.desc = 64, 2048, 2, 2, 128, abi.sf_wq()
+    return w
+
+
+def kv_cache():
+    c = ops.KVCache.__new__(ops.KVCache)
+    c.batch, c.h_kv, c.t_max, c.d, c.desc = 1, 2, 1024, 128, abi.sf_kv()
+    return c
+
+
+# call, what it allocates and hands out, its workspaces
+@pytest.mark.parametrize("call,returned,spaces", [
+    (lambda s, at: weights().gemv(Half(s, 1, 2048), stream=at), 2, 1),
+    (lambda s, at: weights().gemv_split(Half(s, 1, 2048), None, stream=at), 2, 0),
+    (lambda s, at: weights().fit_refinements(Half(s, 64, 2048, dtype=torch.float32), Half(s, 8, 2048), want_delta=True,
+                                             stream=at), 1, 1),
+    (lambda s, at: ops.select_channels(Half(s, 1, 2048), stream=at), 1, 0),
+    (lambda s, at: kv_cache().score_select(Half(s, 1, 8, 128), 100, 4, want_scores=True, stream=at), 3, 1),
+    (lambda s, at: kv_cache().logits_fma(Half(s, 1, 8, 128), 100, stream=at), 1, 1),
+    (lambda s, at: kv_cache().attn_refined(Half(s, 1, 8, 128), 100, None, 4, stream=at), 1, 1),
+    (lambda s, at: kv_cache().attend_selective(Half(s, 1, 8, 128), 100, 4, stream=at), 2, 1),
+], ids=["gemv", "gemv_split", "fit", "select", "score_select", "logits_fma", "attn_refined", "attend_selective"])
+def test_nested_calls_allocate_on_the_stream_that_writes(streams, monkeypatch, call, returned, spaces):
+    for name in vars(abi):
+        if name.startswith("sf_") and not isinstance(getattr(abi, name), type):
+            monkeypatch.setattr(abi, name, lambda *args: 256)
+    monkeypatch.setattr(ops, "check", lambda status, where: None)
+    call(streams, streams.side)
+    assert len(streams.memory) == returned + spaces
+    assert all(t.owner is streams.side for t in streams.memory)
+    assert sum(t.recorded == [streams.main] for t in streams.memory) == returned
+    streams.memory.clear()
+    call(streams, None)
+    assert all(t.owner is streams.main and not t.recorded for t in streams.memory)
