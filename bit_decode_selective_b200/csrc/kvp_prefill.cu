@@ -37,6 +37,7 @@
 // is bounded.
 #include "internal.cuh"
 #include "kvp_attend.cuh"
+#include "kvp_wait.cuh"
 
 namespace sf {
 namespace {
@@ -51,7 +52,6 @@ constexpr int kThreads = (kSoftWarps + kFillWarps + 4) * 32;  // the last warpgr
 constexpr int kSoftRegs = 160, kFillRegs = 56, kIssueRegs = 48;
 constexpr int kRing = 4;                 // steps whose token places are kept
 constexpr float kRefGap = 6.f, kRefShift = 9.f;
-constexpr unsigned long long kWaitNs = 1000000000ull;  // bounded waits give up after 1 s
 constexpr int kMinSteps = 1;             // the fewest steps worth a CTA
 // An item's queries and output take about as long as 4 steps (two prompts of 2,000
 // and 4,001 tokens, window 1,024: 191 us with 4, 207 with 2, 193 with 9).
@@ -91,42 +91,8 @@ __device__ __forceinline__ void regs_down() {
 
 // ---- PTX --------------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Waits for the phase for at most kWaitNs; after one wait of the CTA has given
-// up none waits any more, and the CTA runs to its end without a result.
-__device__ __forceinline__ void mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  const unsigned long long t0 = now_ns();
-  while (!mbar_try(bar, parity)) {
-    if (*gave_up) return;
-    if (now_ns() - t0 > kWaitNs) {
-      *gave_up = 1;
-      atomicAdd(&g_wait_timeouts, 1u);
-      return;
-    }
-  }
-}
 __device__ __forceinline__ void mbar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, gave_up);
+  sf::mbar_wait(bar, parity, gave_up, &g_wait_timeouts);
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -700,8 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) kvp_prefill_kernel(const __grid_c
       } while (advance());
       if (elect_one()) tc_commit(&ctl.last);  // nothing is in flight when TMEM is given back
       __syncwarp();
-      for (unsigned long long t0 = now_ns(); !mbar_try(&ctl.last, 0) && now_ns() - t0 < kWaitNs;) {
-      }
+      mbar_drain(&ctl.last, 0, &g_wait_timeouts);
     }
   }
   tc_before();

@@ -223,7 +223,8 @@ SF_API sf_status sf_gemv_refined_split(const sf_wq* w, const uint16_t* x, int ba
 /* Number of bounded device-side waits that ran out on the current device
  * (*count), optionally reset to 0 (reset != 0).  The refined GEMV waits on
  * shared-memory barriers for its bulk copies, the paged cache's attention for
- * its products; each such wait gives up after one second, counts itself here and lets the kernel finish without its result
+ * its products; each such wait gives up after one second, counts itself here
+ * and lets the kernel finish without its result
  * (the output is then undefined), so a fault in the memory system shows up as
  * a count, not as a hung GPU.  A nonzero count makes this call return
  * SF_ERR_TIMEOUT.  The call synchronises with the device (it reads the counter
