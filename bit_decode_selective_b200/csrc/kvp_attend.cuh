@@ -83,13 +83,15 @@ __device__ __forceinline__ KvpSeq kvp_seq(const KvpAttendArgs& a, int b) {
 }
 
 // The 16-token tiles that queries at positions p0 .. p1 see, in order: `sink`
-// tiles from the start of the sequence, then those from tile `first` on.
+// tiles from the start of the sequence, then those from tile `first` on.  Positions
+// before the sequence see nothing and count as -1: p0 - window stays within 32 bits.
 struct KvpSpan {
   int p0, p1, sink, first, tiles;
   __device__ __forceinline__ int tile(int i) const { return i < sink ? i : i - sink + first; }
 };
 __device__ __forceinline__ KvpSpan kvp_span(const KvpAttendArgs& a, int p0, int p1) {
   KvpSpan s;
+  p0 = max(p0, -1);
   s.p0 = p0, s.p1 = p1;
   const int lo = a.window ? max(0, p0 - a.window + 1) : 0;
   s.first = lo >> 4;
