@@ -152,7 +152,7 @@ struct KvpItem {
 // This CTA's range [u0, u1) of the line (u0 == u1: nothing), and the place `at`
 // on the line of the item where it starts.  The first `more` ranges have size
 // `each` + 1, the others `each`.  The line is counted in 64 bits, but divided in 32:
-// a line past 2^32 steps is cut in larger units.
+// a line of 2^31 steps or more is cut in larger units.
 struct KvpRange {
   long u0, u1, at;
   uint32_t each, more;
@@ -172,11 +172,16 @@ struct KvpRangeShared {
   long at;
   Item it;
 };
+// The KV head whose item holds the step `off` from the first head's start, `each`
+// steps an item: off passes 32 bits only with very many heads and tokens.
+__device__ __forceinline__ int kvp_head_at(long off, int each) {
+  return (int)(off >> 32 ? off / each : (uint32_t)off / (uint32_t)each);
+}
 // The size of the ranges, and this CTA's.  False: it has none.
 __device__ __forceinline__ bool kvp_cut(KvpRange& r, long total, int min_steps) {
   r.u0 = r.u1 = r.at = 0;
   r.unit = 0;
-  while (total >> r.unit >> 32) r.unit++;
+  while (total >> r.unit >> 31) r.unit++;  // at most 2^31 units: nothing below passes 32 bits
   const uint32_t units = (uint32_t)((total + (1l << r.unit) - 1) >> r.unit);
   const uint32_t ctas = min(gridDim.x, (units + min_steps - 1) / min_steps);
   if (blockIdx.x >= ctas) return false;
@@ -232,7 +237,7 @@ __device__ __forceinline__ KvpRange kvp_range_few(const KvpAttendArgs& a, int mi
       const int st = Item::kExtra + Item::steps_of(Item::span_of(a, s, rt));
       const long all = (long)st * a.h_kv;
       if (r.u0 < at + all) {
-        g = (int)((uint32_t)(r.u0 - at) / (uint32_t)st);
+        g = kvp_head_at(r.u0 - at, st);
         at += (long)g * st;
         break;
       }
@@ -294,7 +299,7 @@ __device__ __forceinline__ KvpRange kvp_range(const KvpAttendArgs& a, int min_st
         const long end = SPREAD ? kvp_scan(all) : all;  // inclusive sum over the row tiles at hand
         const bool here = r.u0 >= at + end - all && r.u0 < at + end;
         if (here) {
-          const int g = (int)((uint32_t)(r.u0 - (at + end - all)) / (uint32_t)st);
+          const int g = kvp_head_at(r.u0 - (at + end - all), st);
           sh.it.b = b, sh.it.rt = rt, sh.it.g = g;
           sh.it.seq = s;
           sh.it.set(a);
