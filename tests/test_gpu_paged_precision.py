@@ -78,3 +78,28 @@ def test_few_rows(gain, counts, h_kv, group, d, window, sinks):
     q = rounded(rng.normal(size=(cu[-1], h_kv * group, d)) * gain, "fp16")
     out = seqs.cache.attend(q, i32(seqs.pages), i32(lens), cu_q=i32(cu), window=window, sinks=sinks)
     seqs.check(out, q, cu, "fp16", window, sinks, d ** -0.5, most=64 // group)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("nq", [1, 80])
+def test_values_at_the_limit(dtype, nq):
+    """Values and keys beyond the largest that is stored: fp16 outputs stay finite, as
+    weights rounded up make 65,472 (1 + 2^-11) at most."""
+    rng = np.random.default_rng(nq)
+    n, d = 200, 128
+    k = rng.choice([-1.0, 1.0], (n, 1, d)) * 7e4
+    v = np.full((n, 1, d), 7e4)
+    v[:, :, 1::2] *= -1
+    v[:, :, 64:] = 65408 - rng.integers(0, 2, (n, 1, 64)) * 1000.0
+    cache = PagedKVCache(13, 16, 1, d)
+    cache.write(rounded(k, "fp32"), rounded(v, "fp32"), i32(np.arange(n)))
+    ks, vs = paged.stored(k.astype(np.float32).astype(float)), paged.stored(v.astype(np.float32).astype(float))
+    q = rounded(rng.normal(size=(nq, 4, d)) * 1e-4, dtype)
+    out = cache.attend(q, i32(np.arange(13)[None]), i32([n]))
+    ref, mag, lmag = paged.attend(f64(q), ks, vs, n, 0, 0, d ** -0.5)
+    # keys rounded to fp16 too, as the many-row kernel does
+    delta = lmag * (2.0 ** -11 + 2.0 ** -16) + (lmag + 2) * 2.0 ** -19
+    half = 2.0 ** -11 if dtype == "fp16" else 2.0 ** -8
+    tol = (np.abs(ref) * half + mag * (2.0 ** -10 + np.expm1(2 * delta)[..., None] + (n / 16 + 8) * 17 * 2.0 ** -23)) * (1 + 2.0 ** -6)
+    got = f64(out)
+    assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all()
