@@ -9,10 +9,22 @@ namespace sf {
 namespace {
 
 // Sequences of at most this many rows (queries x query heads per KV head) go to
-// the few-row kernel.
+// the few-row kernel, whose logits are sums of exact products.  Both kernels, in us
+// (few rows | many rows; bf16, 8 KV heads, d = 128):
+//   rows          16           32           40           48           64
+//   1 x 1,024     10 |  16     14 |  16     14 |  16     14 |  17     16 |  17
+//   16 x 1,024    19 |  30     32 |  31     37 |  32     38 |  32     51 |  32
+//   64 x 1,024    46 |  95     81 |  95     98 |  95    101 |  95    135 |  95
+//   1 x 16,384    15 |  34     23 |  35     30 |  36     30 |  36     37 |  36
+//   16 x 16,384  101 | 231    176 | 232    250 | 232    252 | 232    331 | 235
+//   64 x 16,384  362 | 875    634 | 879    934 | 879    937 | 880   1233 | 883
+// So up to 32 rows it is the faster one but for a tie; from there to the limit it is
+// kept for its precision, at up to 1.6 times the other's time for batches of 64 rows each.
 constexpr int kFewRows = 64;
 
-// Rows that a sequence of the few-row kernel is expected to have: the average.
+// The rows by which the few-row kernel's columns are chosen: the average over the
+// call's sequences, all that the host knows.  Long sequences beside single tokens
+// raise it, many single tokens beside a draft lower it; either costs time only.
 int few_rows(int n_q, int batch, int group) {
   const long long rows = ((long long)n_q + batch - 1) / batch * group;
   return rows < kFewRows ? (int)rows : kFewRows;

@@ -160,9 +160,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
   }
 }
 
-// blockIdx: (64 tokens, head, keys or values).  Bound by instructions, 23 per value
-// (a third of them per group, in all four lanes): 8,192 bf16 tokens of 8 heads, 44 MB, in
-// 17 us.  Four CTAs per SM at 64 registers: 10% faster than three at 68.
+// blockIdx: (64 tokens, head, keys or values).  Bound by instructions, 22 per value
+// (a third of them per group, in all four lanes): 8,192 tokens of 8 heads in 16 us
+// (bf16, fp16; 44 MB) or 20 us (fp32; 78 MB).  At d = 128 a thread spills 20 to 24 bytes.  Four CTAs per SM at 64 registers: 10% faster than three at 68.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 4) kvp_write_kernel(const __grid_constant__ CacheArgs a) {
   using L = KvpTile<D>;
@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 4) kvp_write_kernel(const __grid_con
   }
 }
 
-// Bound by HBM: 131,072 tokens of 8 heads to bf16, 705 MB in 120 us = 5.9 TB/s.
+// Bound by HBM: 131,072 tokens of 8 heads to bf16 or fp16, 705 MB in 120 us = 5.9 TB/s;
+// to fp32, 1,242 MB in 274 us = 4.5 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) kvp_read_kernel(const __grid_constant__ CacheArgs a) {
   using L = KvpTile<D>;

@@ -40,13 +40,16 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepTiles = 2;  // tiles per warp and step
 // An item's queries, join and output take about as long as 8 steps of the CTA
-// (64 windows of 1,024 tokens: 32.6 us with 8, 33.5 with 2, 32.9 with 12).
+// (with 2, 8 and 12, bf16: 64 windows of 1,024 tokens 34.2, 33.9, 33.8 us; 100
+// sequences of 200 to 3,000 tokens 64.0, 57.4, 57.5; 200 of 60 to 500, d = 64: 32.5,
+// 27.5, 27.5; 8 of 32,769: 74.0, 72.9, 73.0).
 constexpr int kExtra = 8;
 constexpr float kRefGap = 6.f;   // log2: how far a logit may pass the reference
 constexpr float kRefShift = 9.f; // weights are 2^(x - reference + 9) <= 2^15
 
 // CTAs per SM: three while a thread's sums fit in 168 registers, two beyond (two
-// columns: 27 us against 31 with three CTAs and their spilled registers).
+// columns: 27 us against 31 with three CTAs and their spilled registers).  At d = 128
+// four columns still spill 324 bytes a thread (at d = 64 72 bytes), three 12.
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 constexpr int stages(int nt) { return nt == 4 ? 4 : 3; }  // four rows' columns need the fourth for the exchange
 

@@ -28,10 +28,10 @@
 // exponentials a thread at 8 cycles and warp on the special-function unit, shared
 // by two warps, are 1,700 of them) and products (1,800 for 16 that take 1,034 back
 // to back).  Two tiles in turn keep the tensor cores 45% busy; TMEM has no room for
-// a third.  2,048 bf16 queries of 32 heads (8 KV heads, d = 128) behind 16,384
-// tokens: 0.49 ms = 1.05 PFLOP/s; 8,192 behind 8,192: 0.58 ms = 0.95; 4,096 with a
-// window of 1,024: 0.12 ms = 0.49 (an item's queries, first step and output cost
-// 9 us and are not hidden).
+// a third.  32 bf16 heads (8 KV heads, d = 128): the last 2,048 queries at length
+// 16,384 in 0.505 ms = 1.02 PFLOP/s; a prompt of 8,192 in 0.63 ms = 0.88; one of
+// 4,096 with a window of 1,024 in 0.13 ms = 0.47 (an item's queries, first step and
+// output cost 9 us and are not hidden).
 //
 // The work is cut into equal ranges on the device (kvp_attend.cuh); every wait
 // is bounded.
@@ -48,13 +48,16 @@ constexpr int kTokens = kStep * kKvpTile;
 constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kThreads = (kSoftWarps + kFillWarps + 4) * 32;  // the last warpgroup issues the products
 // Registers per thread: the launch's 96 x 640 threads = 480 x 128, given out anew
-// as (2 x 160 + 2 x 56 + 48) x 128.
+// as (2 x 160 + 2 x 56 + 48) x 128.  The compiler holds all code to the launch's 96
+// and spills 256 bytes a thread at d = 128, 136 at d = 64.
 constexpr int kSoftRegs = 160, kFillRegs = 56, kIssueRegs = 48;
 constexpr int kRing = 4;                 // steps whose token places are kept
 constexpr float kRefGap = 6.f, kRefShift = 9.f;
 constexpr int kMinSteps = 1;             // the fewest steps worth a CTA
-// An item's queries and output take about as long as 4 steps (two prompts of 2,000
-// and 4,001 tokens, window 1,024: 191 us with 4, 207 with 2, 193 with 9).
+// An item's queries and output take about as long as 4 steps (bf16, with 2, 4 and 9:
+// prompts of 2,000 and 4,001 tokens, window 1,024: 205, 180, 178 us; 24 prompts of 300:
+// 114, 110, 112; 2,048 queries at 16,384: 500, 493, 498; 100 queries at five lengths
+// up to 2,000, d = 64: 36, 36, 41).
 constexpr int kExtra = 4;
 
 __device__ unsigned int g_wait_timeouts;

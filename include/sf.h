@@ -451,14 +451,14 @@ SF_API sf_status sf_kvp_read(const sf_kvp* kv, const int32_t* slots, int n, void
  *     sequence; only entries that hold visible tokens are read;
  *   lens [batch] int32 DEVICE: cached tokens per sequence, the queries' own
  *     included.
- *   h_q % h_kv == 0; scale finite; window, sinks >= 0; batch <= 65535;
+ *   h_q % h_kv == 0; scale finite; window, sinks >= 0; 1 <= batch <= 65535;
  *   n_q * h_q < 2^30; out does not overlap q.
  * Device-side arguments are checked there: a length is clamped to [0,
  * max_pages * page], cu_q to [0, n_q], and the tokens of a page index outside
  * [0, n_pages) are not read and not seen; each makes *bad (nullable, a device
  * int32) nonzero.
- * q must be finite, and below 2^100 in magnitude, in every row that is to be
- * finite: a row with a NaN or an infinity spoils its own output only.
+ * q, and scale times q, must be finite and below 2^100 in magnitude in every row
+ * that is to be finite: a row with a NaN or an infinity spoils its own output only.
  * Precision: logits are fp32 sums (of exact products for sequences with at most
  * 64 rows, queries x query heads per KV head; beyond that keys are rounded once
  * to fp16); values and softmax weights are rounded once to fp16, the weights
