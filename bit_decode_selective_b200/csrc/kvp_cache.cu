@@ -162,7 +162,8 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&v)[
 
 // blockIdx: (64 tokens, head, keys or values).  Bound by instructions, 22 per value
 // (a third of them per group, in all four lanes): 8,192 tokens of 8 heads in 16 us
-// (bf16, fp16; 44 MB) or 20 us (fp32; 78 MB).  At d = 128 a thread spills 20 to 24 bytes.  Four CTAs per SM at 64 registers: 10% faster than three at 68.
+// (bf16, fp16; 44 MB) or 20 us (fp32; 78 MB).  Four CTAs per SM at 64 registers, with
+// 20 to 24 bytes a thread spilled at d = 128: 10% faster than three at 68.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 4) kvp_write_kernel(const __grid_constant__ CacheArgs a) {
   using L = KvpTile<D>;

@@ -23,7 +23,9 @@
 //     are split in two fp16).
 //   - Values: (1024 + code) - 1024 and s code + m in fp16 pairs; one rounding of
 //     the value to fp16, as a 16-bit cache would have.  The weights are rounded
-//     to fp16 scaled so that the largest is near 2^15.
+//     to fp16 scaled so that the largest is near 2^15.  (fp16 outputs are then
+//     2.5e-4 to 3.2e-4 from fp64, of which their own rounding is 2.1e-4; to keep
+//     the low halves too would take three products for each of these.)
 //   - ldmatrix reads the tiles as they lie (kvp.cuh); movmatrix turns the
 //     weights from S^T's layout to the operand's.
 //   - The running maximum moves only when some logit passes it by 2^6: then the

@@ -17,8 +17,11 @@
 // hold them; queries are scaled per row by a power of two into fp16's range
 // (exact for fp16 and bf16 but for elements 2^24 below the row's largest);
 // weights are rounded to fp16, scaled so that the largest is near 2^15; sums are
-// fp32.  The softmax reference moves only when a logit passes it by 2^6, so the
-// output sums are hardly ever rescaled.
+// fp32.  (fp16 outputs are then up to 8e-4 from fp64 in relative L2, 2.1e-4 being
+// their own rounding, with keys of which some channels are ten times the others;
+// the low halves of keys, values and weights would take two to three times the
+// products.)  The softmax reference moves only when a logit passes it by 2^6, so
+// the output sums are hardly ever rescaled.
 //
 // Elements of 8 are kept in the order (0 4 1 5 2 6 3 7), the order in which a
 // masked code word gives them up: queries and keys alike, and the output's
@@ -48,8 +51,8 @@ constexpr int kTokens = kStep * kKvpTile;
 constexpr int kSoftWarps = 8, kFillWarps = 8;
 constexpr int kThreads = (kSoftWarps + kFillWarps + 4) * 32;  // the last warpgroup issues the products
 // Registers per thread: the launch's 96 x 640 threads = 480 x 128, given out anew
-// as (2 x 160 + 2 x 56 + 48) x 128.  The compiler holds all code to the launch's 96
-// and spills 256 bytes a thread at d = 128, 136 at d = 64.
+// as (2 x 160 + 2 x 56 + 48) x 128.  ptxas spills 256 bytes a thread at d = 128, 136
+// at d = 64.
 constexpr int kSoftRegs = 160, kFillRegs = 56, kIssueRegs = 48;
 constexpr int kRing = 4;                 // steps whose token places are kept
 constexpr float kRefGap = 6.f, kRefShift = 9.f;

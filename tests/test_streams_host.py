@@ -15,7 +15,8 @@ class Memory:
     """An allocation: the stream it belongs to and the streams it waits for before it is used again."""
 
     def __init__(self, shape, dtype, owner):
-        self.shape, self.dtype, self.owner, self.device = torch.Size(shape) if not isinstance(shape, int) else (shape,), dtype, owner, CPU
+        self.shape = (shape,) if isinstance(shape, int) else torch.Size(shape)
+        self.dtype, self.owner, self.device = dtype, owner, CPU
         self.recorded = []
 
     def data_ptr(self):
